@@ -372,7 +372,7 @@ def _resize(pages, table, lens, new, refs, moves, window, sinks):
     shared = (new > lens) & (lens % BS != 0) & (last >= 0) & (refs[last.clamp(min=0).long()] > 1)
     need = (want - have).clamp(min=0) + shared
     end = need.cumsum(0)
-    ok = end <= free.numel()
+    ok = (end <= free.numel()) | (need == 0)
     first = end - need
     page = lambda k: torch.cat([free, free.new_zeros(1)])[k.clamp(0, free.numel()).long()].to(torch.int32)  # noqa: E731
     col = torch.arange(cols, device=table.device, dtype=torch.int32)[None, :]
@@ -401,7 +401,7 @@ def _fork(pages, table, lens, refs, parent, child, moves):
     tail = table[p].gather(1, full.clamp(max=table.shape[1] - 1).long()[:, None]).squeeze(1)
     need = (part & (tail >= 0)).int()
     end = need.cumsum(0)
-    ok = end <= free.numel()
+    ok = (end <= free.numel()) | (need == 0)
     fresh = torch.cat([free, free.new_zeros(1)])[(end - need).clamp(max=free.numel()).long()].to(torch.int32)
     copy = ok & (need > 0)
     moves[:, 0] = torch.where(copy, tail, -1)
