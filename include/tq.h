@@ -92,6 +92,9 @@ typedef enum {
 #define TQ_DEVERR_TIMEOUT 0x10      /* a bounded wait inside a kernel gave up        */
 #define TQ_DEVERR_LAYOUT 0x20       /* the decode kernel's shared-memory layout did not
                                        match its launch; the launch did nothing      */
+#define TQ_DEVERR_NO_PAGES 0x40     /* too few free pages: a resize or fork was refused */
+#define TQ_DEVERR_SEQ_INDEX 0x80    /* tq_pages_fork: a sequence index outside [0, B), a
+                                       child named twice or not empty, a bad length   */
 
 /* A strided view of a device array.  Strides are in ELEMENTS; shape[i] and
  * stride[i] for i >= ndim are ignored.  data must be aligned to the element size. */
@@ -289,6 +292,116 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
                                          tq_tensor block_table, tq_tensor seq_lens,
                                          const tq_codebooks* cb, uint64_t sign_seed, float scale,
                                          void* stream);
+
+/* Attention of new tokens over the packed pages (this library's own addition next to
+ * tq_paged_decode: the pages describe single-token decode only).  The new tokens' K and V
+ * are already in the pages (tq_quantize_append first); sequence b's new tokens are the last
+ * q_len[b] of its seq_lens[b], so the row of new token i of sequence b stands at position
+ * p = seq_lens[b] - q_len[b] + i and attends to the tokens t <= p with
+ *   window == 0  or  t > p - window  or  t < sinks
+ * (causal; with window > 0 a sliding window plus the first `sinks` tokens):
+ *   out[row, h] = sum_t softmax_t(scale * <q[row,h], k_hat_t>) v_hat_t, k_hat and v_hat as in
+ *   tq_paged_decode.  A row that sees no token (p < 0, an empty sequence) gives 0.
+ *   out, q       [rows, H_q, D] in bf16, f16 or f32 (out: f32 or q's dtype); last dim contiguous.
+ *   q_starts     i32 [B + 1] contiguous, ascending: rows [q_starts[b], q_starts[b+1]) of q and
+ *                out belong to sequence b.  Rows outside [q_starts[0], q_starts[B]) are neither
+ *                read nor written.
+ *   max_q        the largest q_len (host value; it sizes the grid).  A sequence with more new
+ *                tokens, or a range that is not inside [0, rows], raises
+ *                TQ_DEVERR_SEQLEN_RANGE and its rows are left unwritten.
+ *   pages        u8 [num_blocks, 16, H_kv, slot_stride] as tq_quantize_append takes them:
+ *                last dim contiguous, slot_stride >= tq_slot_bytes and a multiple of 8; block,
+ *                row and head strides multiples of 8, data 8-byte aligned.
+ *   block_table  i32 [B, max_blocks], last dim contiguous.  Entries of pages that no row sees
+ *                are not read.  An entry outside [0, num_blocks) raises
+ *                TQ_DEVERR_BLOCK_RANGE and its tokens are skipped.
+ *   seq_lens     i32 [B]; outside [0, max_blocks * 16]: TQ_DEVERR_SEQLEN_RANGE, rows give 0.
+ *   window, sinks  >= 0.
+ * Code widths as in tq_paged_decode (each of 2, 3, 4, 8); D 64, 128 or 256; H_q a multiple of
+ * H_kv, any ratio; block_size 16; H_kv <= 65535 (TQ_ERR_UNSUPPORTED otherwise).
+ * Only tokens a row sees reach its result: whatever the others' norms hold (a stored NaN norm
+ * included).  No workspace, no state between calls: calls may overlap on the GPU, and be captured.
+ * Errors: TQ_ERR_INVALID_ARG / TQ_ERR_UNSUPPORTED (nothing enqueued), TQ_ERR_CUDA. */
+TQ_API tq_status tq_paged_attend(tq_tensor out, tq_tensor q, tq_tensor q_starts, tq_tensor pages,
+                                 tq_tensor block_table, tq_tensor seq_lens,
+                                 const tq_codebooks* cb, uint64_t sign_seed, float scale,
+                                 int32_t max_q, int32_t window, int32_t sinks, void* stream);
+
+/* The single-token form: tq_paged_attend with one new token a sequence (out, q [B, H_q, D]),
+ * window > 0.  Reads the pages of the window and the sinks only, so that the others may have
+ * been released (tq_pages_resize) and their entries be -1. */
+TQ_API tq_status tq_paged_decode_window(tq_tensor out, tq_tensor q, tq_tensor pages,
+                                        tq_tensor block_table, tq_tensor seq_lens,
+                                        const tq_codebooks* cb, uint64_t sign_seed, float scale,
+                                        int32_t window, int32_t sinks, void* stream);
+
+/* Page operations (this library's own addition: the pages describe the page tensor and the
+ * slot mapping, not who hands the pages out).  They keep the block table, the lengths and the
+ * pages' reference counts of a batch on the device, so that a serving loop admits, extends,
+ * forks, cuts and releases sequences without a host round trip.
+ *   layers       host array of num_layers (1..128) page tensors, u8 [num_blocks, 16, H_kv,
+ *                slot_stride] as in tq_paged_decode, all with the same num_blocks: the pools
+ *                of a model's layers, which share one block table (H_kv and slot_stride may
+ *                differ).  A page is contiguous; the stride between pages may be larger (a
+ *                multiple of 16), so that several layers may interleave in one tensor.
+ *                slot_stride a multiple of 8, data 16-byte aligned.
+ *   block_table  i32 [B, max_blocks], last dim contiguous.  -1 marks an entry without a page.
+ *   seq_lens     i32 [B] contiguous.
+ *   ref_counts   i32 [num_blocks] contiguous: how many table entries name the page; 0 = free.
+ *                The caller zeroes it once (and may count pages it keeps for itself).
+ *   moves        i32 [requests, 2] contiguous, written by the call: {from, to} where the
+ *                request got a copy of page `from` in page `to`, {-1, -1} where it needed
+ *                none, {-2, -2} where it was refused.
+ * Free pages are given out lowest index first, in the order of the requests.  A request
+ * that, together with all requests before it, needs more pages than were free when the call
+ * began is refused as a whole and leaves its sequence as it was (TQ_DEVERR_NO_PAGES); pages
+ * released by a call are free for the next one.  Table entries outside [0, num_blocks) raise
+ * TQ_DEVERR_BLOCK_RANGE where a count would change, and are skipped.
+ * Calls that share tables, counts or pages must be ordered on the GPU.  No workspace; nothing
+ * is allocated; every call can be captured.
+ * Limits (TQ_ERR_UNSUPPORTED): num_blocks <= 2^21, B and the number of pairs <= 8192,
+ * max_blocks < 2^26.
+ * Errors: TQ_ERR_INVALID_ARG / TQ_ERR_UNSUPPORTED (nothing enqueued), TQ_ERR_CUDA. */
+
+/* Every sequence b gets new_lens[b] tokens (i32 [B]; equal to seq_lens[b]: unchanged; 0: the
+ * sequence is released), and seq_lens[b] = new_lens[b].
+ *   growing    new entries name free pages.  If the sequence's last page is partly filled and
+ *              shared (count > 1), it is first replaced by a copy of its own, in every layer.
+ *   shrinking  the entries past the new length are released and set to -1.
+ *   window > 0 entries of pages that no query at position min(old, new length) or later can
+ *              see through a sliding window with sinks (tq_paged_attend) are released too and
+ *              set to -1.  The window kernels never read such entries.  0: none.
+ * A length outside [0, max_blocks * 16] raises TQ_DEVERR_SEQLEN_RANGE and leaves the sequence
+ * as it is (moves {-2, -2}).  moves: [B, 2]. */
+TQ_API tq_status tq_pages_resize(const tq_tensor* layers, int32_t num_layers, tq_tensor block_table,
+                                 tq_tensor seq_lens, tq_tensor new_lens, tq_tensor ref_counts,
+                                 tq_tensor moves, int32_t window, int32_t sinks, void* stream);
+
+/* Sequence children[i] becomes a copy of sequence parents[i] (i32 [N] each): it shares the
+ * parent's full pages (their counts go up) and gets its own copy of a partly filled last
+ * page, so that both may append.  Lengths are those at the start of the call.  A child must be
+ * empty (seq_lens 0) and named once; otherwise, or for an index outside [0, B), the pair is
+ * refused with TQ_DEVERR_SEQ_INDEX.  moves: [N, 2]. */
+TQ_API tq_status tq_pages_fork(const tq_tensor* layers, int32_t num_layers, tq_tensor block_table,
+                               tq_tensor seq_lens, tq_tensor ref_counts, tq_tensor parents,
+                               tq_tensor children, tq_tensor moves, void* stream);
+
+/* Gathers kept tokens: token i < counts[b] of sequence b in the pages of dst_table becomes a
+ * copy of its token positions[b, i] in the pages of src_table, in every layer (K and V slots
+ * of all heads).  Any order and repetition; kept tokens in ascending order compact a cache
+ * after eviction, all tokens copy or move a sequence.
+ *   src_table   i32 [B, max_blocks], src_lens i32 [B].
+ *   positions   i32 [B, P], last dim contiguous; counts i32 [B] contiguous.
+ *   dst_table   i32 [B, dst_blocks] (from tq_pages_resize on the destination's tables).
+ * Only rows [0, counts[b]) are written: the rest of the last page stays.  No destination page
+ * may be read by the same call or written twice (its bytes would be unspecified).
+ * A count outside [0, min(P, dst_blocks * 16)] or a source length outside the table raises
+ * TQ_DEVERR_SEQLEN_RANGE and skips the sequence; a position outside [0, src_lens[b]) raises
+ * TQ_DEVERR_SLOT_RANGE, a table entry outside [0, num_blocks) TQ_DEVERR_BLOCK_RANGE, and the
+ * row is skipped.  Lengths and counts are left to the caller. */
+TQ_API tq_status tq_pages_compact(const tq_tensor* layers, int32_t num_layers, tq_tensor src_table,
+                                  tq_tensor src_lens, tq_tensor positions, tq_tensor counts,
+                                  tq_tensor dst_table, void* stream);
 
 /* Workspace bytes tq_paged_decode needs for this geometry (host only).  The
  * workspace holds 2 * batch u32 merge counters at its start (zero between calls:

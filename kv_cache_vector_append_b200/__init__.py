@@ -21,6 +21,13 @@ Public API (names follow the C entry points):
     quantize_append_dense(pages, slot_mapping, k, v, codebooks, rotation, stream=None)
     paged_decode_dense(out, q, pages, block_table, seq_lens, codebooks, rotation, scale, ...)
     rotate_unit_dense(u, norm, x, rotation, stream=None)  # test export of the dense rotation
+    paged_attend(out, q, q_starts, pages, block_table, seq_lens, codebooks, sign_seed, scale,
+                 max_q, window=0, sinks=0)                # chunks of new tokens, causal
+    paged_decode_window(out, q, pages, block_table, seq_lens, codebooks, sign_seed, scale,
+                        window, sinks=0)                  # one token, sliding window and sinks
+    pages_resize(layers, block_table, seq_lens, new_lens, ref_counts, moves, window=0, sinks=0)
+    pages_fork(layers, block_table, seq_lens, ref_counts, parents, children, moves)
+    pages_compact(layers, src_table, src_lens, positions, counts, dst_table)
     decode_workspace_size(...), set_workspace(tensor), get_device_error(stream=None)
 """
 
@@ -29,7 +36,9 @@ from ._binding import (  # noqa: F401
     TQError,
     DEVERR_BLOCK_RANGE,
     DEVERR_NONFINITE,
+    DEVERR_NO_PAGES,
     DEVERR_SEQLEN_RANGE,
+    DEVERR_SEQ_INDEX,
     DEVERR_SLOT_RANGE,
     DEVERR_TIMEOUT,
     debug_inject_merge_stall,
@@ -43,8 +52,13 @@ from ._binding import (  # noqa: F401
     quantize_append_dense,
     paged_decode_dense,
     rotate_unit_dense,
+    pages_compact,
+    pages_fork,
+    pages_resize,
+    paged_attend,
     paged_decode,
     paged_decode_hot,
+    paged_decode_window,
     paged_decode_qjl,
     quantize_append_qjl,
     slot_bytes_qjl,

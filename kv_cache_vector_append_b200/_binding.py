@@ -2,6 +2,7 @@
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -24,6 +25,8 @@ DEVERR_NONFINITE = 0x4
 DEVERR_SEQLEN_RANGE = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_LAYOUT = 0x20
+DEVERR_NO_PAGES = 0x40
+DEVERR_SEQ_INDEX = 0x80
 
 EXPORTED = ("tq_slot_bytes", "tq_quantize_append", "tq_paged_decode", "tq_paged_decode_hot",
             "tq_paged_decode_noalloc",
@@ -31,6 +34,8 @@ EXPORTED = ("tq_slot_bytes", "tq_quantize_append", "tq_paged_decode", "tq_paged_
             "tq_rotate_unit", "tq_decode_plan_probe", "tq_debug_inject_merge_stall",
             "tq_quantize_append_dense", "tq_paged_decode_dense", "tq_rotate_unit_dense",
             "tq_slot_bytes_qjl", "tq_quantize_append_qjl", "tq_paged_decode_qjl",
+            "tq_paged_attend", "tq_paged_decode_window",
+            "tq_pages_resize", "tq_pages_fork", "tq_pages_compact",
             "tq_status_string", "tq_version")
 
 
@@ -76,6 +81,7 @@ def _load():
     lib = ctypes.CDLL(_LIB_PATH)
     T, CB = TensorDesc, ctypes.POINTER(CodebooksDesc)
     RT = ctypes.POINTER(RotationDesc)
+    TP = ctypes.POINTER(TensorDesc)
     sig = {
         "tq_slot_bytes": [ctypes.c_int32] * 3 + [ctypes.POINTER(ctypes.c_int32)],
         "tq_quantize_append": [T, T, T, T, CB, ctypes.c_uint64, ctypes.c_int32, ctypes.c_int32,
@@ -101,6 +107,14 @@ def _load():
                                    ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p],
         "tq_paged_decode_qjl": [T, T, T, T, T, CB, ctypes.c_uint64, ctypes.c_uint64,
                                 ctypes.c_float, ctypes.c_void_p],
+        "tq_paged_attend": [T, T, T, T, T, T, CB, ctypes.c_uint64, ctypes.c_float, ctypes.c_int32,
+                            ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p],
+        "tq_paged_decode_window": [T, T, T, T, T, CB, ctypes.c_uint64, ctypes.c_float,
+                                   ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p],
+        "tq_pages_resize": [TP, ctypes.c_int32, T, T, T, T, T, ctypes.c_int32, ctypes.c_int32,
+                            ctypes.c_void_p],
+        "tq_pages_fork": [TP, ctypes.c_int32, T, T, T, T, T, T, ctypes.c_void_p],
+        "tq_pages_compact": [TP, ctypes.c_int32, T, T, T, T, T, ctypes.c_void_p],
         "tq_status_string": [ctypes.c_int],
     }
     for name, args in sig.items():
@@ -372,6 +386,95 @@ def paged_decode_qjl(out, q, pages, block_table, seq_lens, codebooks: Codebooks,
                                        ctypes.c_uint64(sign_seed), ctypes.c_uint64(qjl_seed),
                                        ctypes.c_float(scale), st),
            "tq_paged_decode_qjl")
+
+
+def _on_device(*tensors):
+    """A context in which the tensors' device (one for all) is the current one."""
+    torch = _torch()
+    _require_cuda(*tensors)
+    device = tensors[0].device
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one device is needed")
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def paged_attend(out, q, q_starts, pages, block_table, seq_lens, codebooks: Codebooks,
+                 sign_seed: int, scale: float, max_q: int, window: int = 0, sinks: int = 0,
+                 stream=None) -> None:
+    """tq_paged_attend: causal attention of each sequence's last tokens (rows q_starts[b] ..
+    q_starts[b + 1] of q, at most max_q) over its packed pages, which hold them already; with
+    window > 0 over the last ``window`` tokens and the first ``sinks`` ones."""
+    with _on_device(out, q, q_starts, pages, block_table, seq_lens, codebooks.k_centroids):
+        st = _stream_handle(stream, q.device)
+        _check(_load().tq_paged_attend(_desc(out), _desc(q), _desc(q_starts), _desc(pages),
+                                       _desc(block_table), _desc(seq_lens),
+                                       ctypes.byref(codebooks.desc), ctypes.c_uint64(sign_seed),
+                                       ctypes.c_float(scale), max_q, window, sinks, st),
+               "tq_paged_attend")
+
+
+def paged_decode_window(out, q, pages, block_table, seq_lens, codebooks: Codebooks,
+                        sign_seed: int, scale: float, window: int, sinks: int = 0,
+                        stream=None) -> None:
+    """tq_paged_decode_window: one new token a sequence over the last ``window`` packed tokens
+    (itself included) and the first ``sinks`` ones."""
+    with _on_device(out, q, pages, block_table, seq_lens, codebooks.k_centroids):
+        st = _stream_handle(stream, q.device)
+        _check(_load().tq_paged_decode_window(_desc(out), _desc(q), _desc(pages),
+                                              _desc(block_table), _desc(seq_lens),
+                                              ctypes.byref(codebooks.desc),
+                                              ctypes.c_uint64(sign_seed), ctypes.c_float(scale),
+                                              window, sinks, st),
+               "tq_paged_decode_window")
+
+
+def _layer_descs(layers):
+    layers = [layers] if hasattr(layers, "data_ptr") else list(layers)
+    if not layers:
+        raise ValueError("no page tensors")
+    return layers, (TensorDesc * len(layers))(*[_desc(t) for t in layers])
+
+
+def pages_resize(layers, block_table, seq_lens, new_lens, ref_counts, moves, window: int = 0,
+                 sinks: int = 0, stream=None) -> None:
+    """tq_pages_resize: give every sequence new_lens[b] tokens: pages for those that grow (a
+    shared, partly filled last page is copied first), entries released for those that shrink,
+    and with window > 0 the pages that a sliding window no longer reaches.  ``layers``: one
+    page tensor, or one a model layer."""
+    layers, descs = _layer_descs(layers)
+    with _on_device(block_table, seq_lens, new_lens, ref_counts, moves, *layers):
+        st = _stream_handle(stream, block_table.device)
+        _check(_load().tq_pages_resize(descs, len(layers), _desc(block_table), _desc(seq_lens),
+                                       _desc(new_lens), _desc(ref_counts), _desc(moves), window,
+                                       sinks, st),
+               "tq_pages_resize")
+
+
+def pages_fork(layers, block_table, seq_lens, ref_counts, parents, children, moves,
+               stream=None) -> None:
+    """tq_pages_fork: the empty sequence children[i] becomes a copy of parents[i]: full pages
+    shared, a partly filled last page copied in every layer."""
+    layers, descs = _layer_descs(layers)
+    with _on_device(block_table, seq_lens, ref_counts, parents, children, moves, *layers):
+        st = _stream_handle(stream, block_table.device)
+        _check(_load().tq_pages_fork(descs, len(layers), _desc(block_table), _desc(seq_lens),
+                                     _desc(ref_counts), _desc(parents), _desc(children),
+                                     _desc(moves), st),
+               "tq_pages_fork")
+
+
+def pages_compact(layers, src_table, src_lens, positions, counts, dst_table, stream=None) -> None:
+    """tq_pages_compact: token i < counts[b] of sequence b in dst_table's pages <- its token
+    positions[b, i] in src_table's pages, in every layer."""
+    layers, descs = _layer_descs(layers)
+    with _on_device(src_table, src_lens, positions, counts, dst_table, *layers):
+        st = _stream_handle(stream, src_table.device)
+        _check(_load().tq_pages_compact(descs, len(layers), _desc(src_table), _desc(src_lens),
+                                        _desc(positions), _desc(counts), _desc(dst_table), st),
+               "tq_pages_compact")
 
 
 def rotate_unit(u, norm, x, sign_seed: int, stream=None) -> None:

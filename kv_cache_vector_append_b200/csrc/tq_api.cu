@@ -10,7 +10,9 @@
 #include <mutex>
 
 #include "tq.h"
+#include "tq_attend_launch.cuh"
 #include "tq_launch.cuh"
+#include "tq_pages_launch.cuh"
 
 namespace tq {
 
@@ -526,6 +528,155 @@ tq_status decode_workspace(const DecodeCall& call, uint8_t** ws) {
   return TQ_OK;
 }
 
+// valid_tensor, but an array without elements may have no data.
+bool valid_array(const tq_tensor& t, int ndim) {
+  if (t.ndim != ndim) return false;
+  for (int i = 0; i < ndim; ++i)
+    if (t.shape[i] < 0) return false;
+  for (int i = 0; i < ndim; ++i)
+    if (t.shape[i] == 0) return dtype_size(t.dtype) != 0;
+  return valid_tensor(t, ndim);
+}
+
+// A contiguous i32 vector of n elements (any length for n < 0).
+bool valid_i32(const tq_tensor& t, int64_t n) {
+  return valid_array(t, 1) && t.dtype == TQ_I32 && (t.shape[0] < 2 || t.stride[0] == 1) &&
+         (n < 0 || t.shape[0] == n);
+}
+bool valid_table(const tq_tensor& t) {
+  return valid_array(t, 2) && t.dtype == TQ_I32 && (t.shape[1] < 2 || t.stride[1] == 1) &&
+         (t.shape[0] < 2 || t.stride[0] >= t.shape[1]);
+}
+bool valid_moves(const tq_tensor& t, int64_t n) {
+  return valid_array(t, 2) && t.dtype == TQ_I32 && t.shape[0] == n && t.shape[1] == 2 &&
+         t.stride[1] == 1 && (n < 2 || t.stride[0] == 2);
+}
+
+// The page tensors of a page operation; *pool receives their common page count.
+tq_status page_layers(const tq_tensor* layers, int32_t n, PageLayers* out, int64_t* pool) {
+  if (layers == nullptr || n < 1) return TQ_ERR_INVALID_ARG;
+  if (n > kMaxPageLayers) return TQ_ERR_UNSUPPORTED;
+  out->count = n;
+  *pool = layers[0].shape[0];
+  for (int i = 0; i < n; ++i) {
+    const tq_tensor& t = layers[i];
+    if (!valid_array(t, 4) || t.dtype != TQ_U8 || t.shape[0] != *pool) return TQ_ERR_INVALID_ARG;
+    if (t.shape[1] != kPageTokens) return TQ_ERR_UNSUPPORTED;
+    if (t.shape[2] < 1 || t.shape[3] < 8 || t.shape[3] % 8 || t.shape[2] > (1 << 20) ||
+        t.shape[3] > (1 << 20))
+      return TQ_ERR_INVALID_ARG;
+    const int64_t row = t.shape[2] * t.shape[3], bytes = row * kPageTokens;
+    if (bytes >= (int64_t)1 << 31) return TQ_ERR_UNSUPPORTED;
+    if (t.stride[3] != 1 || (t.shape[2] > 1 && t.stride[2] != t.shape[3]) || t.stride[1] != row ||
+        (*pool > 1 && (t.stride[0] < bytes || t.stride[0] % 16)) || (uintptr_t)t.data % 16)
+      return TQ_ERR_INVALID_ARG;
+    out->base[i] = (uint8_t*)t.data;
+    out->blk_stride[i] = t.stride[0];
+    out->page_bytes[i] = (int32_t)bytes;
+  }
+  return *pool > kMaxPoolPages ? TQ_ERR_UNSUPPORTED : TQ_OK;
+}
+
+constexpr int64_t kMaxTableCols = (int64_t)1 << 26;
+
+// Validation and parameters of the attention over chunks and windows (q_starts null: one
+// row a sequence).
+tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* q_starts,
+                     const tq_tensor& pages, const tq_tensor& block_table,
+                     const tq_tensor& seq_lens, const tq_codebooks* cb, uint64_t sign_seed,
+                     float scale, int32_t max_q, int32_t window, int32_t sinks, void* stream) {
+  if (cb == nullptr || !std::isfinite(scale) || max_q < 0 || window < 0 || sinks < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!valid_array(q, 3) || !is_float_dtype(q.dtype) || q.stride[2] != 1) return TQ_ERR_INVALID_ARG;
+  if (!valid_array(out, 3) || out.stride[2] != 1 || (out.dtype != TQ_F32 && out.dtype != q.dtype))
+    return TQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (out.shape[i] != q.shape[i]) return TQ_ERR_INVALID_ARG;
+  if (!valid_array(pages, 4) || pages.dtype != TQ_U8 || pages.stride[3] != 1)
+    return TQ_ERR_INVALID_ARG;
+  const int64_t B = block_table.shape[0];
+  if (!valid_table(block_table) || !valid_i32(seq_lens, B)) return TQ_ERR_INVALID_ARG;
+  if (q_starts != nullptr ? !valid_i32(*q_starts, B + 1) : q.shape[0] != B) return TQ_ERR_INVALID_ARG;
+  const int64_t h_q = q.shape[1], D = q.shape[2], h_kv = pages.shape[2];
+  if (h_kv < 1 || h_q < 1 || h_q % h_kv) return TQ_ERR_INVALID_ARG;
+  if (!valid_codebook(cb->k, (int)D) || !valid_codebook(cb->v, (int)D)) return TQ_ERR_INVALID_ARG;
+  const int kb = region_bytes((int)D, cb->k.bits), vb = region_bytes((int)D, cb->v.bits);
+  if (pages.shape[3] < kb + vb || pages.shape[3] % 8 || pages.stride[0] % 8 ||
+      pages.stride[1] % 8 || pages.stride[2] % 8 || (uintptr_t)pages.data % 8)
+    return TQ_ERR_INVALID_ARG;
+  if (pages.shape[1] != kBlockSize || (D != 64 && D != 128 && D != 256) ||
+      !decode_bits_supported(cb->k.bits, cb->v.bits) || h_kv > 65535 || h_q > (1 << 20) ||
+      q.shape[0] > 0x7fffffff || pages.shape[0] > 0x7fffffff || B > (1 << 24) ||
+      block_table.shape[1] >= kMaxTableCols || pages.stride[2] > 0x7fffffff)
+    return TQ_ERR_UNSUPPORTED;
+  max_q = (int32_t)std::min<int64_t>(max_q, q.shape[0]);
+  const int64_t group = h_q / h_kv;
+  if ((max_q * group + 7) / 8 > 65535) return TQ_ERR_UNSUPPORTED;   // row tiles: a grid dimension
+  if (B == 0 || q.shape[0] == 0) return TQ_OK;
+  DeviceState* ds = nullptr;
+  const tq_status s = device_state(&ds);
+  if (s != TQ_OK) return s;
+  AttendParams p{};
+  p.pages = (const uint8_t*)pages.data;
+  p.num_blocks = (int32_t)pages.shape[0];
+  p.h_kv = (int32_t)h_kv;
+  p.slot_stride = (int32_t)pages.stride[2];
+  p.row_stride = pages.stride[1];
+  p.blk_stride = pages.stride[0];
+  p.block_table = (const int32_t*)block_table.data;
+  p.bt_stride = block_table.stride[0];
+  p.max_blocks = (int32_t)block_table.shape[1];
+  p.seq_lens = (const int32_t*)seq_lens.data;
+  p.batch = (int32_t)B;
+  p.q_starts = q_starts != nullptr ? (const int32_t*)q_starts->data : nullptr;
+  p.num_rows = (int32_t)q.shape[0];
+  p.max_q = std::max(max_q, 1);
+  p.q = q.data;
+  p.q_rstride = q.stride[0];
+  p.q_hstride = q.stride[1];
+  p.q_dtype = q.dtype;
+  p.out = out.data;
+  p.o_rstride = out.stride[0];
+  p.o_hstride = out.stride[1];
+  p.out_dtype = out.dtype;
+  p.group = (int32_t)group;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.sign_seed = sign_seed;
+  p.kc = cb->k.centroids;
+  p.vc = cb->v.centroids;
+  p.k_region = kb;
+  p.window = window;
+  p.sinks = sinks;
+  p.err = ds->err.load(std::memory_order_relaxed);
+  p.wait_ms = kWaitMs;
+  return launch_attend_any((int)D, cb->k.bits, cb->v.bits, p, ds->info, as_stream(stream));
+}
+
+// What resize and fork have in common.
+tq_status plan_params(const tq_tensor* layers, int32_t num_layers, const tq_tensor& block_table,
+                      const tq_tensor& seq_lens, const tq_tensor& ref_counts,
+                      const tq_tensor& moves, int64_t requests, PageLayers* pl, PlanParams* p) {
+  int64_t pool = 0;
+  const tq_status s = page_layers(layers, num_layers, pl, &pool);
+  if (s != TQ_OK) return s;
+  if (!valid_table(block_table) || !valid_i32(seq_lens, block_table.shape[0]) ||
+      !valid_i32(ref_counts, pool) || !valid_moves(moves, requests))
+    return TQ_ERR_INVALID_ARG;
+  if (block_table.shape[0] > kMaxPageRequests || requests > kMaxPageRequests ||
+      block_table.shape[1] >= kMaxTableCols)
+    return TQ_ERR_UNSUPPORTED;
+  p->table = (int32_t*)block_table.data;
+  p->table_stride = block_table.stride[0];
+  p->cols = (int32_t)block_table.shape[1];
+  p->seq_lens = (int32_t*)seq_lens.data;
+  p->batch = (int32_t)block_table.shape[0];
+  p->requests = (int32_t)requests;
+  p->refs = (int32_t*)ref_counts.data;
+  p->pool = (int32_t)pool;
+  p->moves = (int32_t*)moves.data;
+  return TQ_OK;
+}
+
 }  // namespace
 }  // namespace tq
 
@@ -995,6 +1146,99 @@ tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor pages,
   // counters at zero; the partial records a launch reads are written earlier in the
   // same launch.
   return decode_run(call, out, q, pages, block_table, seq_lens, cb, sign_seed, scale, ws, stream);
+}
+
+tq_status tq_paged_attend(tq_tensor out, tq_tensor q, tq_tensor q_starts, tq_tensor pages,
+                          tq_tensor block_table, tq_tensor seq_lens, const tq_codebooks* cb,
+                          uint64_t sign_seed, float scale, int32_t max_q, int32_t window,
+                          int32_t sinks, void* stream) {
+  return attend_run(out, q, &q_starts, pages, block_table, seq_lens, cb, sign_seed, scale, max_q,
+                    window, sinks, stream);
+}
+
+tq_status tq_paged_decode_window(tq_tensor out, tq_tensor q, tq_tensor pages,
+                                 tq_tensor block_table, tq_tensor seq_lens,
+                                 const tq_codebooks* cb, uint64_t sign_seed, float scale,
+                                 int32_t window, int32_t sinks, void* stream) {
+  if (window < 1) return TQ_ERR_INVALID_ARG;
+  return attend_run(out, q, nullptr, pages, block_table, seq_lens, cb, sign_seed, scale, 1, window,
+                    sinks, stream);
+}
+
+tq_status tq_pages_resize(const tq_tensor* layers, int32_t num_layers, tq_tensor block_table,
+                          tq_tensor seq_lens, tq_tensor new_lens, tq_tensor ref_counts,
+                          tq_tensor moves, int32_t window, int32_t sinks, void* stream) {
+  PageLayers pl;
+  PlanParams p{};
+  tq_status s = plan_params(layers, num_layers, block_table, seq_lens, ref_counts, moves,
+                            block_table.shape[0], &pl, &p);
+  if (s != TQ_OK) return s;
+  if (!valid_i32(new_lens, p.batch) || window < 0 || sinks < 0) return TQ_ERR_INVALID_ARG;
+  if (p.batch == 0) return TQ_OK;
+  DeviceState* ds = nullptr;
+  s = device_state(&ds);
+  if (s != TQ_OK) return s;
+  p.new_lens = (const int32_t*)new_lens.data;
+  p.window = window;
+  p.sinks = sinks;
+  p.err = ds->err.load(std::memory_order_relaxed);
+  return launch_pages_resize(p, pl, ds->info, as_stream(stream));
+}
+
+tq_status tq_pages_fork(const tq_tensor* layers, int32_t num_layers, tq_tensor block_table,
+                        tq_tensor seq_lens, tq_tensor ref_counts, tq_tensor parents,
+                        tq_tensor children, tq_tensor moves, void* stream) {
+  PageLayers pl;
+  PlanParams p{};
+  tq_status s = plan_params(layers, num_layers, block_table, seq_lens, ref_counts, moves,
+                            parents.shape[0], &pl, &p);
+  if (s != TQ_OK) return s;
+  if (!valid_i32(parents, -1) || !valid_i32(children, parents.shape[0])) return TQ_ERR_INVALID_ARG;
+  if (p.requests == 0) return TQ_OK;
+  DeviceState* ds = nullptr;
+  s = device_state(&ds);
+  if (s != TQ_OK) return s;
+  p.parents = (const int32_t*)parents.data;
+  p.children = (const int32_t*)children.data;
+  p.err = ds->err.load(std::memory_order_relaxed);
+  return launch_pages_fork(p, pl, ds->info, as_stream(stream));
+}
+
+tq_status tq_pages_compact(const tq_tensor* layers, int32_t num_layers, tq_tensor src_table,
+                           tq_tensor src_lens, tq_tensor positions, tq_tensor counts,
+                           tq_tensor dst_table, void* stream) {
+  PageLayers pl;
+  int64_t pool = 0;
+  tq_status s = page_layers(layers, num_layers, &pl, &pool);
+  if (s != TQ_OK) return s;
+  if (!valid_table(src_table) || !valid_table(dst_table) || !valid_table(positions))
+    return TQ_ERR_INVALID_ARG;
+  const int64_t B = src_table.shape[0];
+  if (!valid_i32(src_lens, B) || !valid_i32(counts, B) || dst_table.shape[0] != B ||
+      positions.shape[0] != B)
+    return TQ_ERR_INVALID_ARG;
+  if (B > kMaxPageRequests || src_table.shape[1] >= kMaxTableCols ||
+      dst_table.shape[1] >= kMaxTableCols || positions.shape[1] > 0x7fffffff - kPageTokens)
+    return TQ_ERR_UNSUPPORTED;
+  if (B == 0 || positions.shape[1] == 0) return TQ_OK;
+  DeviceState* ds = nullptr;
+  s = device_state(&ds);
+  if (s != TQ_OK) return s;
+  CompactParams p{};
+  p.src_table = (const int32_t*)src_table.data;
+  p.src_stride = src_table.stride[0];
+  p.src_cols = (int32_t)src_table.shape[1];
+  p.src_lens = (const int32_t*)src_lens.data;
+  p.positions = (const int32_t*)positions.data;
+  p.pos_stride = positions.stride[0];
+  p.max_keep = (int32_t)positions.shape[1];
+  p.counts = (const int32_t*)counts.data;
+  p.dst_table = (const int32_t*)dst_table.data;
+  p.dst_stride = dst_table.stride[0];
+  p.dst_cols = (int32_t)dst_table.shape[1];
+  p.pool = (int32_t)pool;
+  p.err = ds->err.load(std::memory_order_relaxed);
+  return launch_pages_compact(p, pl, (int)B, as_stream(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,73 @@
+// tq_attend_launch.cuh -- host-side launch of the attention over chunks and windows.
+#pragma once
+
+#include "tq_attend_rows.cuh"
+#include "tq_launch.cuh"
+
+namespace tq {
+
+template <int D, int KB, int VB>
+tq_status launch_rows_t(const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
+  auto kern = attend_rows_kernel<D, KB, VB>;
+  constexpr int smem = rows_smem(D, KB, VB);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  // CTAs a cluster: enough for two CTAs an SM, as long as each warp keeps two pages or more
+  const int tiles = (int)(((int64_t)p.max_q * p.group + kRowsMax - 1) / kRowsMax);
+  int64_t steps = p.max_blocks;
+  if (p.window > 0)
+    steps = std::min(steps, ((int64_t)p.window + p.max_q - 1) / kBlockSize + 2 +
+                                ((int64_t)p.sinks + kBlockSize - 1) / kBlockSize);
+  const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
+  int ctas = 1;
+  while (ctas < kRowsMaxCtas && groups * ctas < 2 * di.num_sms &&
+         (int64_t)ctas * kRowsWarps * 4 <= steps)
+    ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.batch * ctas), (unsigned)p.h_kv, (unsigned)tiles);
+  cfg.blockDim = dim3(kRowsWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return TQ_ERR_CUDA;
+  return launch_status();
+}
+
+// All V widths for one (head_dim, K width); instantiated in tq_attend_d<D>_k<KB>.cu so that
+// the kernels compile in parallel.
+template <int D, int KB>
+tq_status launch_rows_kbits(int vb, const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
+  switch (vb) {
+    case 2: return launch_rows_t<D, KB, 2>(p, di, st);
+    case 3: return launch_rows_t<D, KB, 3>(p, di, st);
+    case 4: return launch_rows_t<D, KB, 4>(p, di, st);
+    case 8: return launch_rows_t<D, KB, 8>(p, di, st);
+    default: return TQ_ERR_UNSUPPORTED;
+  }
+}
+
+#define TQ_DECLARE_ROWS(D_, KB_)                                                          \
+  tq_status launch_rows_d##D_##_k##KB_(int vb, const AttendParams& p, const DeviceInfo& di, \
+                                       cudaStream_t st);
+#define TQ_DEFINE_ROWS(D_, KB_)                                                           \
+  tq_status launch_rows_d##D_##_k##KB_(int vb, const AttendParams& p, const DeviceInfo& di, \
+                                       cudaStream_t st) {                                  \
+    return launch_rows_kbits<D_, KB_>(vb, p, di, st);                                      \
+  }
+TQ_FOR_EACH_DECODE(TQ_DECLARE_ROWS)
+
+inline tq_status launch_attend_any(int dim, int kb, int vb, const AttendParams& p,
+                                   const DeviceInfo& di, cudaStream_t st) {
+#define TQ_ROWS_CASE(D_, KB_) \
+  if (dim == D_ && kb == KB_) return launch_rows_d##D_##_k##KB_(vb, p, di, st);
+  TQ_FOR_EACH_DECODE(TQ_ROWS_CASE)
+#undef TQ_ROWS_CASE
+  return TQ_ERR_UNSUPPORTED;
+}
+
+}  // namespace tq

@@ -1,0 +1,431 @@
+// tq_pages.cuh -- page operations of a packed cache on device tables: give and take pages
+// (resize), share them with another sequence (fork), gather kept tokens (compact).
+//
+// State.  ref_counts[page] = number of block-table entries that name the page; a page is
+// free when its count is 0.  Pages are given out lowest index first, to the requests in
+// their order, so the result does not depend on how the grid runs.
+//
+// resize and fork are two launches.  The first (one cluster) decides and allocates: it
+// turns the counts into a bitmap of free pages in shared memory (each CTA a contiguous
+// part of the pool), joins the CTAs' totals over distributed shared memory, and lets
+// thread r of the demanded ranks find its page (a search in the prefix sums of the
+// bitmap's words, then the n-th set bit) and its request (a search in the prefix sums of
+// the demands).  The second (one CTA per sequence and layer) does what is long: page
+// copies, shared or released table entries, count updates (integer atomics, so their
+// order does not matter).  What the second needs to know of the first is in `moves`, a
+// tensor of the caller: {from, to} of a page copy, {-1, -1} for none, {-2, -2} for a
+// refused request.  No other state is kept between the launches or the calls.
+//
+// Bound: the first launch by latency (a few dependent reads and cluster barriers; the
+// pool is read once), the second and compact by memory bandwidth.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "tq_device.cuh"
+
+namespace tq {
+
+constexpr int kPageTokens = 16;            // tokens per page block
+constexpr int kMaxPageLayers = 128;        // pools one call copies pages of
+constexpr int kMaxPageRequests = 8192;     // sequences of the table, pairs of a fork
+constexpr int kMaxPoolPages = 1 << 21;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxCtas = 8;            // portable cluster size
+constexpr int kPagesThreads = 256;
+
+// The pools that a call moves slots in (one per model layer).
+struct PageLayers {
+  int32_t count;
+  uint8_t* base[kMaxPageLayers];
+  int64_t blk_stride[kMaxPageLayers];      // bytes between pages
+  int32_t page_bytes[kMaxPageLayers];      // a multiple of 128
+};
+
+struct PlanParams {
+  int32_t* table;                          // [batch, cols]
+  int64_t table_stride;
+  int32_t cols;
+  int32_t* seq_lens;
+  int32_t batch;
+  const int32_t* new_lens;                 // resize
+  const int32_t* parents;                  // fork [requests]
+  const int32_t* children;
+  int32_t requests;
+  int32_t* refs;                           // [pool]
+  int32_t pool;
+  int32_t* moves;                          // [requests, 2]
+  int32_t window, sinks;                   // resize: pages out of the window are released
+  unsigned int* err;
+};
+
+// Bitmap words of one CTA's part of the pool.
+__host__ __device__ inline int plan_words(int pool, int ctas) {
+  return ((pool + 31) / 32 + ctas - 1) / ctas;
+}
+// Shared memory of the plan: bitmap, its prefix sums, the demands' prefix sums, lengths and
+// kinds, and (fork) the first pair of each child.
+inline size_t plan_smem(int pool, int ctas, int requests, int owners) {
+  return 4 * ((size_t)2 * plan_words(pool, ctas) + 2 + 2 * (size_t)requests + owners) + requests;
+}
+
+// Exclusive prefix sums over the block of one value a thread; *total receives the sum.
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* warp_sums, unsigned* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();                         // warp_sums of an earlier scan are read
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    unsigned w = warp_sums[lane];          // kPlanThreads / 32 = 32 warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned t = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += t;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return inc - v + (warp ? warp_sums[warp - 1] : 0u);
+}
+
+// The largest i in [0, n) with a[i] <= x (a[0] <= x, a ascending).
+__device__ __forceinline__ int last_not_above(const unsigned* a, int n, unsigned x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__host__ __device__ __forceinline__ int pages_of(int tokens) {
+  return tokens / kPageTokens + (tokens % kPageTokens != 0);
+}
+
+// What a request asks for: its pages, the length they are for, and its kind.
+enum : uint8_t { kAsksNothing = 0, kAsksPages = 1, kAsksCopy = 2, kBadRequest = 4 };
+struct Demand {
+  int pages;
+  int len;
+  uint8_t kind;
+};
+
+// A growing sequence asks for the pages past its last one, and for one more, the first, where
+// its partly filled last page is shared (copy on write).
+__device__ __forceinline__ Demand resize_demand(const PlanParams& p, int b) {
+  const int len = p.seq_lens[b], to = p.new_lens[b];
+  const int64_t room = (int64_t)p.cols * kPageTokens;
+  if (len < 0 || len > room || to < 0 || to > room) return Demand{0, 0, kBadRequest};
+  Demand d{0, len, kAsksNothing};
+  if (to <= len) return d;
+  if (len % kPageTokens) {
+    const int last = p.table[b * p.table_stride + len / kPageTokens];
+    if (last >= 0 && last < p.pool && p.refs[last] > 1) d.kind |= kAsksCopy;
+  }
+  d.pages = pages_of(to) - pages_of(len) + ((d.kind & kAsksCopy) ? 1 : 0);
+  if (d.pages) d.kind |= kAsksPages;
+  return d;
+}
+
+// A fork asks for a page of its own where its parent's last page is partly filled.
+// owner[c]: the first pair that names child c.
+__device__ __forceinline__ Demand fork_demand(const PlanParams& p, int i, const int* owner) {
+  const int from = p.parents[i], to = p.children[i];
+  if (from < 0 || from >= p.batch || to < 0 || to >= p.batch || owner[to] != i)
+    return Demand{0, 0, kBadRequest};
+  const int len = p.seq_lens[from];
+  if (p.seq_lens[to] != 0 || len < 0 || len > (int64_t)p.cols * kPageTokens)
+    return Demand{0, 0, kBadRequest};
+  Demand d{0, len, kAsksNothing};
+  if (len % kPageTokens) {
+    const int last = p.table[from * p.table_stride + len / kPageTokens];
+    if (last >= 0 && last < p.pool) {
+      d.kind = kAsksPages | kAsksCopy;
+      d.pages = 1;
+    }
+  }
+  return d;
+}
+
+template <bool FORK>
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PlanParams p) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int words = plan_words(p.pool, ctas);
+  extern __shared__ __align__(16) uint32_t plan_mem[];
+  uint32_t* bitmap = plan_mem;                       // [words] free pages of this CTA's part
+  unsigned* before = plan_mem + words;               // [words + 1] free pages before a word
+  unsigned* need = before + words + 1;               // [requests + 1] pages asked before a request
+  int* lens = (int*)(need + p.requests + 1);         // [requests]
+  int* owner = lens + p.requests;                    // [batch] (fork)
+  uint8_t* kind = (uint8_t*)(owner + (FORK ? p.batch : 0));   // [requests]
+  __shared__ unsigned warp_sums[32];
+  __shared__ unsigned cta_free;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int word0 = rank * words;
+
+  // free pages of this part: one ballot a word
+  for (int w = tid >> 5; w < words; w += kPlanThreads / 32) {
+    const int64_t page = (int64_t)(word0 + w) * 32 + lane;
+    const uint32_t bits = __ballot_sync(0xffffffffu, page < p.pool && p.refs[page] == 0);
+    if (lane == 0) bitmap[w] = bits;
+  }
+  if (FORK) {
+    for (int b = tid; b < p.batch; b += kPlanThreads) owner[b] = 0x7fffffff;
+    __syncthreads();
+    for (int i = tid; i < p.requests; i += kPlanThreads) {
+      const int to = p.children[i];
+      if (to >= 0 && to < p.batch) atomicMin(&owner[to], i);
+    }
+  }
+  __syncthreads();
+  unsigned carry = 0;
+  for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
+    const int w = w0 + tid;
+    unsigned total;
+    const unsigned pre = block_scan(w < words ? __popc(bitmap[w]) : 0, warp_sums, &total);
+    if (w < words) before[w] = carry + pre;
+    carry += total;
+  }
+  if (tid == 0) {
+    before[words] = carry;
+    cta_free = carry;
+  }
+  // the demands (every CTA: they are few next to the pool).  One above the pool counts as
+  // pool + 1 and the sums stop at 2^30, which is refused all the same.
+  constexpr unsigned kCap = 1u << 30;
+  unsigned asked = 0;
+  for (int i0 = 0; i0 < p.requests; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    Demand d{0, 0, kAsksNothing};
+    if (i < p.requests) {
+      d = FORK ? fork_demand(p, i, owner) : resize_demand(p, i);
+      lens[i] = d.len;
+      kind[i] = d.kind;
+    }
+    unsigned total;
+    const unsigned pre = block_scan((unsigned)min(d.pages, p.pool + 1), warp_sums, &total);
+    if (i < p.requests) need[i] = min(asked + pre, kCap);
+    asked = min(asked + total, kCap);
+  }
+  if (tid == 0) need[p.requests] = asked;
+  cluster.sync();        // the counts and lengths are read by every CTA, the totals are there
+  unsigned first = 0, free_pages = 0;
+  for (int c = 0; c < ctas; ++c) {
+    const unsigned n = *cluster.map_shared_rank(&cta_free, c);
+    if (c < rank) first += n;
+    free_pages += n;
+  }
+  // the ranks [first, first + carry) of the demand are served from this part
+  const unsigned end = min(first + carry, asked);
+  for (unsigned r = first + tid; r < end; r += kPlanThreads) {
+    const int i = last_not_above(need, p.requests + 1, r);
+    if (need[i + 1] > free_pages) continue;          // refused as a whole
+    const int w = last_not_above(before, words + 1, r - first);
+    const int page = (word0 + w) * 32 + (int)__fns(bitmap[w], 0, (int)(r - first - before[w]) + 1);
+    const int k = (int)(r - need[i]);
+    p.refs[page] = 1;
+    const int seq = FORK ? p.children[i] : i;
+    const int copies = (kind[i] & kAsksCopy) ? 1 : 0;
+    int32_t* row = p.table + seq * p.table_stride;
+    if (k < copies) {
+      const int col = lens[i] / kPageTokens;
+      const int from = p.table[(FORK ? p.parents[i] : seq) * p.table_stride + col];
+      p.moves[2 * i] = from;
+      p.moves[2 * i + 1] = page;
+      row[col] = page;
+    } else {
+      row[pages_of(lens[i]) + k - copies] = page;
+    }
+  }
+  if (rank == 0) {
+    for (int i = tid; i < p.requests; i += kPlanThreads) {
+      const uint8_t what = kind[i];
+      const bool bad = what & kBadRequest;
+      const bool refused = (what & kAsksPages) && need[i + 1] > free_pages;
+      if (bad) report_error(p.err, FORK ? TQ_DEVERR_SEQ_INDEX : TQ_DEVERR_SEQLEN_RANGE);
+      if (refused) report_error(p.err, TQ_DEVERR_NO_PAGES);
+      if (bad || refused || !(what & kAsksCopy)) {
+        const int mark = bad || refused ? -2 : -1;
+        p.moves[2 * i] = mark;
+        p.moves[2 * i + 1] = mark;
+      }
+      if (FORK && !bad && !refused) p.seq_lens[p.children[i]] = lens[i];
+    }
+  }
+  cluster.sync();        // no CTA leaves while another may read its total
+}
+
+// 16-byte units [0, bytes) of one page copied by the block, four loads in flight a thread.
+__device__ __forceinline__ void copy_page(const PageLayers& l, int layer, int from, int to) {
+  const uint4* s = (const uint4*)(l.base[layer] + from * l.blk_stride[layer]);
+  uint4* d = (uint4*)(l.base[layer] + to * l.blk_stride[layer]);
+  const int n = l.page_bytes[layer] / 16;
+  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kPagesThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * kPagesThreads < n) v[j] = s[i0 + j * kPagesThreads];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * kPagesThreads < n) d[i0 + j * kPagesThreads] = v[j];
+  }
+}
+
+// Second launch of resize: grid (batch, 1 + layers).  CTA (b, 0) releases sequence b's
+// entries and gives it its length, CTA (b, 1 + l) makes its page copy in layer l.
+static __global__ void __launch_bounds__(kPagesThreads)
+pages_resize_kernel(const PlanParams p, const __grid_constant__ PageLayers layers) {
+  const int b = blockIdx.x;
+  const int from = p.moves[2 * b], to = p.moves[2 * b + 1];
+  if (from == -2) return;
+  if (blockIdx.y > 0) {
+    if (from >= 0) copy_page(layers, blockIdx.y - 1, from, to);
+    return;
+  }
+  const int len = p.seq_lens[b], want = p.new_lens[b];
+  const int have = pages_of(len), keep = pages_of(want), least = min(len, want);
+  int32_t* row = p.table + b * p.table_stride;
+  // pages no query at a position >= least sees: all tokens >= sinks and < least - window + 1
+  const int w0 = p.window > 0 ? pages_of(p.sinks) : 0;
+  const int w1 = p.window > 0 ? max(0, least - p.window + 1) / kPageTokens : 0;
+  auto release = [&](int c) {
+    const int id = row[c];
+    if (id < 0) return;
+    if (id < p.pool) atomicSub(&p.refs[id], 1);
+    else report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
+    row[c] = -1;
+  };
+  for (int c = w0 + threadIdx.x; c < min(w1, min(have, keep)); c += kPagesThreads) release(c);
+  for (int c = keep + threadIdx.x; c < have; c += kPagesThreads) release(c);
+  __syncthreads();                         // the old length has been read
+  if (threadIdx.x == 0) {
+    if (from >= 0) atomicSub(&p.refs[from], 1);
+    p.seq_lens[b] = want;
+  }
+}
+
+constexpr int kForkChunk = 4 * kPagesThreads;   // table entries a CTA shares
+
+// Second launch of fork: grid (pairs, chunks of the table row + layers).  The entries of the
+// parent's full pages are shared with the child, its partly filled one is copied.
+static __global__ void __launch_bounds__(kPagesThreads)
+pages_fork_kernel(const PlanParams p, const __grid_constant__ PageLayers layers, int chunks) {
+  const int i = blockIdx.x;
+  const int from = p.moves[2 * i], to = p.moves[2 * i + 1];
+  if (from == -2) return;
+  if ((int)blockIdx.y >= chunks) {
+    if (from >= 0) copy_page(layers, blockIdx.y - chunks, from, to);
+    return;
+  }
+  const int child = p.children[i];
+  const int len = p.seq_lens[child];       // the parent's before the call
+  const int32_t* src = p.table + p.parents[i] * p.table_stride;
+  int32_t* dst = p.table + child * p.table_stride;
+  // a partly filled last page without a copy is a hole (or out of range) in the parent too
+  const int end = from >= 0 ? len / kPageTokens : pages_of(len);
+  const int c0 = blockIdx.y * kForkChunk;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = c0 + j * kPagesThreads + threadIdx.x;
+    if (c >= end) break;
+    const int id = src[c];
+    dst[c] = id;
+    if (id >= 0) {
+      if (id < p.pool) atomicAdd(&p.refs[id], 1);
+      else report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
+    }
+  }
+}
+
+struct CompactParams {
+  const int32_t* src_table;
+  int64_t src_stride;
+  int32_t src_cols;
+  const int32_t* src_lens;
+  const int32_t* positions;                // [batch, max_keep]
+  int64_t pos_stride;
+  int32_t max_keep;
+  const int32_t* counts;
+  const int32_t* dst_table;
+  int64_t dst_stride;
+  int32_t dst_cols;
+  int32_t pool;
+  unsigned int* err;
+};
+
+// Rows [0, counts[b]) of sequence b in the destination pages <- its rows positions[b, .].
+// One CTA per destination page, sequence and layer: its 16 rows' addresses are resolved
+// once, then their U-byte units are copied with four loads in flight a thread.
+template <typename U>
+__global__ void __launch_bounds__(kPagesThreads)
+pages_compact_kernel(const CompactParams p, const __grid_constant__ PageLayers layers) {
+  const int b = blockIdx.y, layer = blockIdx.z;
+  const int count = p.counts[b], len = p.src_lens[b];
+  if (count < 0 || count > p.max_keep || pages_of(count) > p.dst_cols || len < 0 ||
+      len > (int64_t)p.src_cols * kPageTokens) {
+    if (threadIdx.x == 0) report_error(p.err, TQ_DEVERR_SEQLEN_RANGE);
+    return;
+  }
+  const int i0 = blockIdx.x * kPageTokens;
+  if (i0 >= count) return;
+  const int rows = min(kPageTokens, count - i0);
+  const int row_units = layers.page_bytes[layer] / kPageTokens / (int)sizeof(U);
+  __shared__ const U* src[kPageTokens];
+  __shared__ U* dst_page;
+  if ((int)threadIdx.x < rows) {
+    const int t = p.positions[b * p.pos_stride + i0 + threadIdx.x];
+    const U* s = nullptr;
+    if (t < 0 || t >= len) {
+      report_error(p.err, TQ_DEVERR_SLOT_RANGE);
+    } else {
+      const int id = p.src_table[b * p.src_stride + t / kPageTokens];
+      if (id < 0 || id >= p.pool) report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
+      else s = (const U*)(layers.base[layer] + id * layers.blk_stride[layer]) +
+               (t % kPageTokens) * row_units;
+    }
+    src[threadIdx.x] = s;
+  }
+  if (threadIdx.x == 32) {
+    const int id = p.dst_table[b * p.dst_stride + blockIdx.x];
+    if (id < 0 || id >= p.pool) {
+      report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
+      dst_page = nullptr;
+    } else {
+      dst_page = (U*)(layers.base[layer] + id * layers.blk_stride[layer]);
+    }
+  }
+  __syncthreads();
+  U* d = dst_page;
+  if (d == nullptr) return;
+  const int n = rows * row_units;
+  for (int u0 = threadIdx.x; u0 < n; u0 += 4 * kPagesThreads) {
+    U v[4];
+    bool ok[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int u = u0 + j * kPagesThreads;
+      ok[j] = false;
+      if (u < n) {
+        const int r = u / row_units;
+        const U* s = src[r];
+        ok[j] = s != nullptr;
+        if (ok[j]) v[j] = s[u - r * row_units];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (ok[j]) d[u0 + j * kPagesThreads] = v[j];
+  }
+}
+
+}  // namespace tq
