@@ -146,26 +146,30 @@ def _torch():
     return torch
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    table = {torch.uint8: U8, torch.int32: I32, torch.int64: I64, torch.float32: F32,
-             torch.bfloat16: BF16, torch.float16: F16}
-    if t.dtype not in table:
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.uint8: U8, torch.int32: I32, torch.int64: I64,
+                             torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return table[t.dtype]
+    return code
+
+
+# TensorDesc of each rank as one pack (several times faster than filling its fields)
+_PACK = [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack for n in range(5)]
 
 
 def _desc(t) -> TensorDesc:
-    if t.dim() > 4:
+    shape = t.shape
+    n = len(shape)
+    if n > 4:
         raise ValueError("tensors of rank > 4 are not supported")
-    d = TensorDesc()
-    d.data = t.data_ptr()
-    d.dtype = _dtype_code(t)
-    d.ndim = t.dim()
-    for i in range(t.dim()):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
-    return d
+    return TensorDesc.from_buffer_copy(_PACK[n](t.data_ptr(), _dtype_code(t), n, *shape, *t.stride()))
 
 
 def _stream_handle(stream, device):
@@ -388,17 +392,20 @@ def paged_decode_qjl(out, q, pages, block_table, seq_lens, codebooks: Codebooks,
            "tq_paged_decode_qjl")
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _on_device(*tensors):
     """A context in which the tensors' device (one for all) is the current one."""
     torch = _torch()
     _require_cuda(*tensors)
-    device = tensors[0].device
+    index = tensors[0].get_device()
     for t in tensors:
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}: one device is needed")
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        if t.get_device() != index:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device is needed")
+    if index == torch.cuda.current_device():
+        return _NO_CONTEXT
+    return torch.cuda.device(index)
 
 
 def paged_attend(out, q, q_starts, pages, block_table, seq_lens, codebooks: Codebooks,
