@@ -39,6 +39,7 @@ struct AttendParams {
   const float* vc;
   int32_t k_region;             // bytes of the K region (offset of the V region)
   int32_t window, sinks;
+  int32_t tile_rows;            // rows a CTA of the tiles kernel takes
   unsigned int* err;
   uint32_t wait_ms;
 };

@@ -1,0 +1,6 @@
+// Tile attention kernels for head_dim 128 with 3-bit K codes.
+#include "tq_attend_launch.cuh"
+
+namespace tq {
+TQ_DEFINE_TILES(128, 3)
+}
