@@ -20,7 +20,7 @@
 // warpgroups (a thread = a row: scores from tensor memory, P back over them), warps 8-11 turn
 // packed codes into fp16 tiles in shared memory (lookups of code pairs, one 256-byte row an
 // entry, so that 32 lanes hit 32 banks; the next tile's codes are already on their way into
-// registers), warp 12 issues the MMAs: P V of an item, then Q K of the slot's next one, so that
+// registers), warps 12 and 13 issue the MMAs: P V of an item, then Q K of the slot's next one, so that
 // one slot's softmax runs under the other's MMAs.  Both operand tiles are rows of 64 columns with
 // the 128-byte swizzle: K-major for Q K, MN-major for P V, the same bytes.  A cluster of CTAs
 // may split the keys; partials are joined over distributed shared memory as in the rows kernel.
@@ -37,10 +37,11 @@
 namespace tq {
 
 constexpr int kTileRows = 128;             // rows of a slot (the MMA's M)
-constexpr int kTilesThreads = 512;
+constexpr int kTilesThreads = 512, kTilesWarps = kTilesThreads / 32;
+constexpr int kDequantWarps = 4;
 constexpr int kTilesMaxCtas = 8;
 // registers a thread of the softmax, dequantizing and issuing warpgroups, from kTilesRegs each
-constexpr int kTilesRegs = 128, kSoftmaxRegs = 168, kDequantRegs = 104, kIssueRegs = 72;
+constexpr int kTilesRegs = 128, kSoftmaxRegs = 152, kDequantRegs = 128, kIssueRegs = 80;
 static_assert(2 * kSoftmaxRegs + kDequantRegs + kIssueRegs <= 4 * kTilesRegs, "registers of a CTA");
 
 template <int D, int KB, int VB, bool PREC>
@@ -55,39 +56,53 @@ struct TilesCfg {
   static constexpr int N = STAGE / (2 * D * KPARTS);
   static constexpr int RING = D == 256 && PREC ? 2 : 3;
   static constexpr int PPT = N / kBlockSize;             // pages a tile
+  // A slot works on items of NI keys of a tile, two score buffers in turn
+  static constexpr int NI = N < 64 ? N : 64, H = N / NI;
   static constexpr int QTILE = kTileRows * D * 2;        // one part of one row tile
   static constexpr int QBYTES = (kTwoTiles ? 2 : 1) * QPARTS * QTILE;
   static constexpr int PART = D + 4;                     // floats of a row's partial
   static constexpr int STAGING = (kOneO ? 1 : 2) * kTileRows * PART * 4;
   static constexpr int OPER = QBYTES + RING * STAGE > STAGING ? QBYTES + RING * STAGE : STAGING;
   static constexpr int LUT = kLutRow * (lut_entries(KB) > lut_entries(VB) ? lut_entries(KB) : lut_entries(VB));
-  static constexpr int NORMS = 2 * N * 2 * 4;
-  static constexpr int MISC = 512;
+  // norms [buffer][K, V][N]; a row tile whose key tiles alternate uses four buffers, at D <= 128
+  // without PREC in the place of the second row tile's q
+  static constexpr int NBUF = PREC || !kOneO ? 2 : 4;
+  static constexpr int NORMS = NBUF * N * 2 * 4;
+  static constexpr int MISC = 896;
   // more than half an SM: a CTA that holds all of tensor memory has the SM to itself
   static constexpr int RAW = OPER + LUT + NORMS + MISC;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
   // dequantization: 16 codes a lane
-  static constexpr int LPR = D / 16, RPI = 32 / LPR, IT = N / 4 / RPI;
-  static_assert(N % 16 == 0 && N <= 128 && IT >= 1 && N / 4 % RPI == 0, "tile geometry");
+  static constexpr int LPR = D / 16, RPI = 32 / LPR, IT = N / kDequantWarps / RPI;
+  // codes of both kinds a whole tile ahead in registers, or of the next kind only
+  static constexpr int KW = KB == 2 ? 1 : KB == 8 ? 4 : 2, VW = VB == 2 ? 1 : VB == 8 ? 4 : 2;
+  static constexpr bool kDeep = IT * (KW + VW) <= 32;
+  static_assert(N % 16 == 0 && N <= 128 && IT >= 1 && N / kDequantWarps % RPI == 0, "tile geometry");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// Per-tile facts, one entry a dequantizing warp (its N / 4 keys).
+// What the dequantizing warps know of their N / 4 keys of a tile: bounds of log2 of the norms,
+// and whether every row of the CTA sees every key and all norms are finite.
 struct TileMeta {
-  float emax, emin;                        // bounds of log2 nV
-  int plain;                               // every row of the CTA sees every key, finite norms
+  int kmax, kmin, vmax, vmin, plain;
+};
+// And of the whole tile.  plain: no masks, V norms within 2^8 of each other; without PREC also
+// K norms, and the operands then hold nK 2^-ek c and nV 2^-ev c, else c alone.
+struct TileInfo {
+  int plain;
+  float ek_scale;                          // 2^ek
+  float ev;
 };
 
 struct TilesMisc {
-  uint64_t s_full[2], p_ready[2], norm_full[2], ring_full[3], ring_empty[3], o_done;
-  uint32_t tmem;
-  int dead;
-  float alpha[2];
-  int tok[2][8];                           // first token of a page of the tile; < 0: no page
-  TileMeta meta[2][4];
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2], norm_full[4], ring_full[3], ring_empty[3], o_done;
   unsigned long long best[2];
+  uint32_t tmem;
+  int tok[4][8];                           // first token of a page of the tile; < 0: no page
+  TileMeta meta[2][kDequantWarps];
+  TileInfo info[4];
 };
-static_assert(sizeof(TilesMisc) <= 512, "misc area");
+static_assert(sizeof(TilesMisc) <= 896, "misc area");
 
 __device__ __forceinline__ void umma_ts_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -152,6 +167,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R)); }
 template <int R>
@@ -176,20 +196,78 @@ struct Codes16 {
   }
 };
 
-// Lookup tables of the tiles: entry e at row e, K in the first half of a row, V in the second,
-// one copy a lane.  BITS <= 4: half2 of a code pair; 8 bits: half2(hi, lo) of a code.
-template <int BITS, int HALF>
-__device__ __forceinline__ void tiles_lut(uint8_t* lut, const float* c, float alpha, int tid) {
-  for (int i = tid; i < lut_entries(BITS) * 32; i += kTilesThreads) {
-    const int e = i >> 5, l = i & 31;
-    uint32_t v;
-    if constexpr (BITS <= 4) {
-      v = pack_half2(c[e & ((1 << BITS) - 1)] * alpha, c[e >> BITS] * alpha);
-    } else {
-      const float hi = __half2float(__float2half_rn(c[e]));
-      v = pack_half2(hi, c[e] - hi);
+// E consecutive elements at element off; vec: the run is aligned to its size (16 bytes at most).
+template <int E>
+__device__ __forceinline__ void load_run(float (&x)[E], const void* base, int64_t off, int32_t dtype, bool vec) {
+  if (vec && dtype != TQ_F32) {
+    uint32_t w[E / 2];
+    const uint32_t* a = (const uint32_t*)((const uint16_t*)base + off);
+    if constexpr (E == 2) w[0] = *a;
+    else if constexpr (E == 4) *(uint2*)w = *(const uint2*)a;
+    else *(uint4*)w = *(const uint4*)a;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      if (dtype == TQ_BF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*(const __half2*)&w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
     }
-    *(uint32_t*)(lut + e * kLutRow + HALF * 128 + 4 * l) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = load_as_f32(base, off + i, dtype);
+  }
+}
+template <int E>
+__device__ __forceinline__ void store_run(const float (&x)[E], void* base, int64_t off, int32_t dtype, bool vec) {
+  if (vec && dtype != TQ_F32) {
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      if (dtype == TQ_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *(const uint32_t*)&h;
+      } else {
+        w[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+      }
+    }
+    uint32_t* a = (uint32_t*)((uint16_t*)base + off);
+    if constexpr (E == 2) *a = w[0];
+    else if constexpr (E == 4) *(uint2*)a = *(const uint2*)w;
+    else *(uint4*)a = *(const uint4*)w;
+  } else if (vec) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) *(float2*)((float*)base + off + i) = make_float2(x[i], x[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) store_from_f32(base, off + i, dtype, x[i]);
+  }
+}
+
+// Lookup tables of the tiles: entry e at row e, K in the first half of a row, V in the second,
+// one copy a lane.  BITS <= 4: half2 of a code pair; 8 bits: half2(hi, lo) of a code.  A warp
+// makes 32 entries at a time, one a lane, and writes each to its row.
+template <int BITS, int HALF>
+__device__ __forceinline__ void tiles_lut(uint8_t* lut, const float* c, float alpha, int warp, int lane) {
+  constexpr int kEntries = lut_entries(BITS);
+  for (int e0 = warp * 32; e0 < kEntries; e0 += kTilesThreads) {
+    const int e = e0 + lane;
+    uint32_t v = 0u;
+    if (e < kEntries) {
+      if constexpr (BITS <= 4) {
+        v = pack_half2(c[e & ((1 << BITS) - 1)] * alpha, c[e >> BITS] * alpha);
+      } else {
+        const float hi = __half2float(__float2half_rn(c[e]));
+        v = pack_half2(hi, c[e] - hi);
+      }
+    }
+    uint32_t* row = (uint32_t*)(lut + e0 * kLutRow + HALF * 128) + lane;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < kEntries) row[j * (kLutRow / 4)] = __shfl_sync(0xffffffffu, v, j);
   }
 }
 // The factor whose scaled centroids lie nearest to fp16 numbers: 1 + best / 512.
@@ -212,12 +290,32 @@ __device__ __forceinline__ void tiles_alpha(const float* c, int tid, unsigned lo
   }
 }
 
+// mbar_wait for waits that are usually short: some polls before the clock is read.
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, uint32_t limit_ms) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 i;\n mov.u32 i, 0;\n"
+      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " add.u32 i, i, 1;\n setp.lt.u32 q, i, 256;\n @q bra POLL;\n"
+      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (done) return true;
+  return mbar_wait(bar, parity, limit_ms);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+
 template <int D, int KB, int VB, bool PREC>
 __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const AttendParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   using C = TilesCfg<D, KB, VB, PREC>;
-  constexpr int N = C::N, PART = C::PART, E = D / 32;
+  constexpr int N = C::N, NI = C::NI, PART = C::PART, E = D / 32;
   constexpr int KPACK = D * KB / 8, VPACK = D * VB / 8;
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* q_s = smem;                                   // [row tile][part][64-column blocks]
@@ -245,24 +343,31 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   const int k_begin = (int)((int64_t)all_tiles * split / ctas);
   const int tiles = (int)((int64_t)all_tiles * (split + 1) / ctas) - k_begin;
   const bool two = C::kTwoTiles && rows > kTileRows;     // two row tiles, else key tiles alternate
-  const int items = two ? 2 * tiles : tiles;
+  // tiles of slot j, and its i-th
+  auto slot_tiles = [&](int j) { return two || C::kOneO ? (C::kOneO && j ? 0 : tiles) : (tiles + 1 - j) / 2; };
+  auto slot_tile = [&](int j, int i) { return two || C::kOneO ? i : 2 * i + j; };
 
   if (smem_u32(smem) & 1023u) {                          // the same in every CTA of the kernel
     if (tid == 0) report_error(p.err, TQ_DEVERR_LAYOUT);
     return;
   }
+  // One thread issues the MMAs of a slot, in the order P V (n - 2), Q K (n); a shared O' has one
+  // thread for all.
+  constexpr int kIssuers = C::kOneO ? 1 : 2;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms->s_full[i], 1);
-      mbar_init(&ms->p_ready[i], kTileRows);
-      mbar_init(&ms->norm_full[i], 128);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&ms->s_full[i][j], 1);
+        mbar_init(&ms->p_ready[i][j], 4);                // a warp's arrival each
+      }
+      mbar_init(&ms->pv_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&ms->norm_full[i], kDequantWarps);
     for (int i = 0; i < C::RING; ++i) {
-      mbar_init(&ms->ring_full[i], 128);
-      mbar_init(&ms->ring_empty[i], 1);
+      mbar_init(&ms->ring_full[i], kDequantWarps);
+      mbar_init(&ms->ring_empty[i], two ? 2 : 1);
     }
-    mbar_init(&ms->o_done, 1);
-    ms->dead = 0;
+    mbar_init(&ms->o_done, kIssuers);
     ms->best[0] = ms->best[1] = ~0ull;
     fence_mbar_init();
   }
@@ -270,8 +375,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  tiles_alpha<KB>(p.kc, tid, &ms->best[0]);
-  tiles_alpha<VB>(p.vc, tid, &ms->best[1]);
+  if constexpr (PREC) {
+    tiles_alpha<KB>(p.kc, tid, &ms->best[0]);
+    tiles_alpha<VB>(p.vc, tid, &ms->best[1]);
+  }
   // q' of a row by a warp: sign flips, FWHT, 1/sqrt(D), to unit length, fp16 (hi, lo)
   {
     uint32_t sgn[E];
@@ -280,15 +387,19 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       sgn[i] = sign_mask_at(p.sign_seed, lane * E + i) ^ (p.scale_log2 < 0.f ? 0x80000000u : 0u);
     constexpr int B = 4;
     const int all = two ? 2 * kTileRows : kTileRows;
-    for (int rb = warp * B; rb < all; rb += 16 * B) {
+    for (int rb = warp * B; rb < all; rb += kTilesWarps * B) {
       float x[B][E];
 #pragma unroll
       for (int j = 0; j < B; ++j) {
         const int r = rb + j, rr = r0 + r;
         const int64_t off = (int64_t)(sq.row0 + rr / G) * p.q_rstride +
                             (int64_t)(kvh * G + rr % G) * p.q_hstride + lane * E;
+        if (r < rows) {
+          load_run<E>(x[j], p.q, off, p.q_dtype, p.q_vec);
+        } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[j][i] = r < rows ? load_as_f32(p.q, off + i, p.q_dtype) : 0.f;
+          for (int i = 0; i < E; ++i) x[j][i] = 0.f;
+        }
       }
 #pragma unroll
       for (int j = 0; j < B; ++j) {
@@ -329,10 +440,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     }
   }
   __syncthreads();                                       // the best factors are known
-  const float ak = KB <= 4 ? 1.0f + (float)(unsigned)ms->best[0] * (1.0f / kTilesThreads) : 1.0f;
-  const float av = VB <= 4 ? 1.0f + (float)(unsigned)ms->best[1] * (1.0f / kTilesThreads) : 1.0f;
-  tiles_lut<KB, 0>(lut, p.kc, ak, tid);
-  tiles_lut<VB, 1>(lut, p.vc, av, tid);
+  const float ak = PREC && KB <= 4 ? 1.0f + (float)(unsigned)ms->best[0] * (1.0f / kTilesThreads) : 1.0f;
+  const float av = PREC && VB <= 4 ? 1.0f + (float)(unsigned)ms->best[1] * (1.0f / kTilesThreads) : 1.0f;
+  tiles_lut<KB, 0>(lut, p.kc, ak, warp, lane);
+  tiles_lut<VB, 1>(lut, p.vc, av, kTilesWarps - 1 - warp, lane);
   const int srow = tid & (kTileRows - 1);                // a softmax thread's row in its slot
   float qs = 0.f;
   int myrow = srow;
@@ -343,63 +454,71 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   fence_proxy_async_smem();                              // q is read by the tensor cores
   __syncthreads();
   const uint32_t tmem = ms->tmem;
-  constexpr uint32_t O_COL = 0, S_COL = 256;
-  // O' of slot j at columns j D (D <= 128), its scores and weights at 256 + 128 j
+  // tensor memory: O' of slot j at columns j D, its scores (and weights) at 256 + 128 j, 64 a buffer
   auto fail = [&]() {
     report_error(p.err, TQ_DEVERR_TIMEOUT);
-    ms->dead = 1;
   };
+  // norm buffers
+  float* norms = C::NBUF == 2 && !PREC && !two ? (float*)(q_s + C::QTILE) : norm_s;
+  const int nmask = PREC || two ? 1 : 3, nshift = PREC || two ? 1 : 2;
   // ring position of a tile's K and V
   auto k_at = [&](int k) { return two ? 2 * k : (k == 0 ? 0 : 2 * k - 1); };
   auto v_at = [&](int k) { return two ? 2 * k + 1 : 2 * k + 2; };
 
   if (warp >= 12) {
     regs_dec<kIssueRegs>();
-    if (warp == 12 && lane == 0 && items > 0) {
+    // The whole warp walks the loop, so that descriptors stay in uniform registers; one thread
+    // issues.
+    const int uwarp = __shfl_sync(0xffffffffu, warp, 0);
+    if (uwarp < 12 + kIssuers && tiles > 0) {
+      const bool leader = elect_one();
+      const int slot = uwarp - 12, items = slot_tiles(slot) * C::H;
+      const uint32_t acc = tmem + slot * D, s_at = tmem + 256 + slot * 128;
+      const uint64_t q = sw128_desc(smem_u32(q_s) + (two ? slot * C::QPARTS * C::QTILE : 0));
+      const uint32_t ring_at = smem_u32(ring_s);
       bool ok = true;
-      for (int n = 0; n < items + 2 && ok; ++n) {
+      for (int n = 0; n < items + 2; ++n) {
         if (n >= 2) {                                    // P V of item n - 2
-          const int m = n - 2, k = two ? m >> 1 : m, at = v_at(k), sl = at % C::RING;
-          ok = mbar_wait(&ms->p_ready[m & 1], (uint32_t)(m >> 1) & 1u, p.wait_ms) &&
-               mbar_wait(&ms->ring_full[sl], (uint32_t)(at / C::RING) & 1u, p.wait_ms);
-          if (!ok) break;
+          const int m = n - 2, at = v_at(slot_tile(slot, m / C::H)), sl = at % C::RING, half = m % C::H;
+          ok = (half || tile_wait(&ms->ring_full[sl], (uint32_t)(at / C::RING) & 1u, p.wait_ms)) &&
+               tile_wait(&ms->p_ready[slot][m & 1], (uint32_t)(m >> 1) & 1u, p.wait_ms);
+          if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
-          const uint32_t vb = smem_u32(ring_s + sl * C::STAGE);
-          const uint32_t acc = tmem + O_COL + (C::kOneO ? 0 : (m & 1) * D);
-          const bool first = C::kOneO ? m == 0 : m < 2;
+          const uint64_t v = sw128_mn_desc(ring_at + sl * C::STAGE, N * 128) + half * (NI * 8);
+          const uint32_t pw = s_at + (m & 1) * 64;
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < N / 16; ++ks)
-            umma_ts_f16(acc, tmem + S_COL + (m & 1) * 128 + ks * 8,
-                        sw128_mn_desc(vb + ks * 2048, N * 128), f16_idesc(D, true),
-                        (ks > 0 || !first) ? 1u : 0u);
-          if (!two || (m & 1)) umma_commit(&ms->ring_empty[sl]);
+            for (int ks = 0; ks < NI / 16; ++ks)         // 16 keys: 2048 bytes of each block
+              umma_ts_f16(acc, pw + ks * 8, v + ks * 128, f16_idesc(D, true), (ks > 0 || m > 0) ? 1u : 0u);
+            umma_commit(&ms->pv_done[slot]);
+            if (half == C::H - 1) umma_commit(&ms->ring_empty[sl]);
+          }
         }
         if (n < items) {                                 // Q K of item n
-          const int k = two ? n >> 1 : n, at = k_at(k), sl = at % C::RING;
-          if (!two || !(n & 1)) ok = mbar_wait(&ms->ring_full[sl], (uint32_t)(at / C::RING) & 1u, p.wait_ms);
-          if (!ok) break;
+          const int at = k_at(slot_tile(slot, n / C::H)), sl = at % C::RING, half = n % C::H;
+          ok = half || tile_wait(&ms->ring_full[sl], (uint32_t)(at / C::RING) & 1u, p.wait_ms);
+          if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
-          const uint32_t kb = smem_u32(ring_s + sl * C::STAGE);
-          const uint32_t qb = smem_u32(q_s + (two ? (n & 1) * C::QPARTS * C::QTILE : 0));
-          const uint32_t acc = tmem + S_COL + (n & 1) * 128;
+          const uint64_t kd = sw128_desc(ring_at + sl * C::STAGE) + half * (NI * 8);
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t qo = (ks >> 2) * (kTileRows * 128) + (ks & 3) * 32;
-            const uint32_t ko = (ks >> 2) * (N * 128) + (ks & 3) * 32;
-            umma_bf16(acc, sw128_desc(qb + qo), sw128_desc(kb + ko), f16_idesc(N, false), ks > 0 ? 1u : 0u);
-            if constexpr (PREC)
-              umma_bf16(acc, sw128_desc(qb + C::QTILE + qo), sw128_desc(kb + ko), f16_idesc(N, false), 1u);
-            if constexpr (C::kKeyLo)
-              umma_bf16(acc, sw128_desc(qb + qo), sw128_desc(kb + (D / 64) * (N * 128) + ko),
-                        f16_idesc(N, false), 1u);
+            for (int ks = 0; ks < D / 16; ++ks) {        // 16 coordinates: 32 bytes of a block
+              const uint64_t qd = q + (ks >> 2) * (kTileRows * 8) + (ks & 3) * 2;
+              const uint64_t ko = kd + (ks >> 2) * (N * 8) + (ks & 3) * 2;
+              const uint32_t to = s_at + (n & 1) * 64;
+              umma_bf16(to, qd, ko, f16_idesc(NI, false), ks > 0 ? 1u : 0u);
+              if constexpr (PREC) umma_bf16(to, qd + C::QTILE / 16, ko, f16_idesc(NI, false), 1u);
+              if constexpr (C::kKeyLo) umma_bf16(to, qd, ko + (D / 64) * (N * 8), f16_idesc(NI, false), 1u);
+            }
+            umma_commit(&ms->s_full[slot][n & 1]);
+            if (half == C::H - 1) umma_commit(&ms->ring_empty[sl]);
           }
-          umma_commit(&ms->s_full[n & 1]);
-          if (!two || (n & 1)) umma_commit(&ms->ring_empty[sl]);
         }
       }
-      umma_commit(&ms->o_done);
-      ok = mbar_wait(&ms->o_done, 0, p.wait_ms) && ok;   // what was issued is complete
-      if (!ok) fail();
+      __syncwarp();
+      if (leader) umma_commit(&ms->o_done);
+      ok = tile_wait(&ms->o_done, 0, p.wait_ms) && ok;   // what was issued is complete
+      if (!ok && leader) fail();
     }
     __syncwarp();
   } else if (warp >= 8) {
@@ -407,15 +526,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     regs_dec<kDequantRegs>();
     const int w = warp - 8;
     const int l = lane % C::LPR, rsub = lane / C::LPR;
-    const int rbase = w * (N / 4) + rsub;                // this lane's rows: rbase + i RPI
+    const int rbase = w * (N / kDequantWarps) + rsub;                // this lane's rows: rbase + i RPI
     const int low_last = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos_last - p.window + 1) : 0;
     const int64_t head = (int64_t)kvh * p.slot_stride;
-    uint32_t raw[C::IT][4];
     // The pages of this warp's rows, WP a tile: a lane holds one table entry of a window of TW
     // tiles (and one of the next window), so that no entry is waited for.
-    constexpr int WP = N / 4 > kBlockSize ? N / 4 / kBlockSize : 1, TW = 32 / WP;
+    constexpr int NW = N / kDequantWarps;                // a warp's rows of a tile
+    constexpr int WP = NW > kBlockSize ? NW / kBlockSize : 1, TW = 32 / WP;
     auto entry = [&](int k) -> int32_t {                 // this lane's entry of the window at tile k
-      const int step = (k_begin + k + lane / WP) * C::PPT + w * (N / 4) / kBlockSize + lane % WP;
+      const int step = (k_begin + k + lane / WP) * C::PPT + w * NW / kBlockSize + lane % WP;
       if (k + lane / WP >= tiles || step >= steps) return -1;
       const int32_t id = p.block_table[(int64_t)b * p.bt_stride + span.at(step)];
       if (id >= 0 && id < p.num_blocks) return id;
@@ -423,49 +542,51 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       return -1;
     };
     int32_t window = entry(0), window_next = entry(TW);
-    struct Bases {
-      const uint8_t* at[WP];
+    struct Pages {
+      int32_t id[WP];
     };
     auto fetch = [&](int k) {                            // of tiles 0, 1, 2, ... in turn
       if (k > 0 && k % TW == 0) {
         window = window_next;
         window_next = entry(k + TW);
       }
-      Bases r;
+      Pages r;
 #pragma unroll
-      for (int j = 0; j < WP; ++j) {
-        const int32_t id = __shfl_sync(0xffffffffu, window, (k % TW) * WP + j);
-        r.at[j] = id < 0 ? nullptr : p.pages + (int64_t)id * p.blk_stride + head;
-      }
+      for (int j = 0; j < WP; ++j) r.id[j] = __shfl_sync(0xffffffffu, window, (k % TW) * WP + j);
       return r;
     };
-    // Rows i of a unit from its pages: this lane's first row of page j at at[j]
+    auto base_of = [&](int32_t id) -> const uint8_t* {
+      return id < 0 ? nullptr : p.pages + (int64_t)id * p.blk_stride + head;
+    };
+    // Rows i of a unit from its pages, in turn (at: this lane's next row)
+    constexpr int IPP = C::IT / WP;                      // rows of a lane in a page
     const int64_t row_step = C::RPI * p.row_stride;
     const int64_t lane_at = (int64_t)(rbase % kBlockSize) * p.row_stride;
-    constexpr int IPP = C::IT / WP;                      // rows of a lane in a page
-    auto load_rows = [&](auto IV, uint32_t (&r)[4], int i, const Bases& from, const uint8_t*& at) {
+    auto load_rows = [&](auto IV, auto& raw, int i, const Pages& from, const uint8_t*& at) {
       constexpr bool V = decltype(IV)::value;
       if (i % IPP == 0) {
-        at = from.at[i / IPP];
+        at = base_of(from.id[i / IPP]);
         if (at != nullptr) at += lane_at + (V ? p.k_region : 0);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = 0u;
+      uint32_t r[4] = {0u, 0u, 0u, 0u};
       if (at != nullptr) {
         if constexpr (V) Codes16<VB>::load(r, at, l);
         else Codes16<KB>::load(r, at, l);
         at += row_step;
       }
+#pragma unroll
+      for (int j = 0; j < (V ? C::VW : C::KW); ++j) raw[i][j] = r[j];
     };
     auto look = [&](uint32_t a) { return *(const uint32_t*)(lut + a); };
     const uint32_t lk = 4u * lane, lv = 128u + 4u * lane;
-    // 16 codes to 16 halves, stored as two 16-byte chunks of the row; the order in which a
-    // lane stores its two keeps 8 lanes on 8 chunks
-    auto store_one = [&](auto IV, auto IL, const uint32_t (&r)[4], int i, uint8_t* stage) {
+    // 16 codes to 16 halves
+    auto look_up = [&](auto IV, auto IL, const auto& raw, int i, uint32_t (&h)[8]) {
       constexpr bool V = decltype(IV)::value, LO = decltype(IL)::value;
-      constexpr int BITS = V ? VB : KB;
+      constexpr int BITS = V ? VB : KB, W = V ? C::VW : C::KW;
       const uint32_t off = V ? lv : lk;
-      uint32_t h[8];
+      uint32_t r[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) r[j] = raw[i][j];
       static_for<8>([&](auto JI) {
         constexpr int j = decltype(JI)::value;
         if constexpr (BITS <= 4) {
@@ -475,6 +596,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
                              look(lut_addr<(2 * j + 1) * BITS, BITS>(r, off)), LO ? 0x7632 : 0x5410);
         }
       });
+    };
+    // ... stored as two 16-byte chunks of the row; the order in which a lane stores its two
+    // keeps 8 lanes on 8 chunks
+    auto store_row = [&](auto IL, const uint32_t (&h)[8], int i, uint8_t* stage) {
+      constexpr bool LO = decltype(IL)::value;
       const int row = rbase + i * C::RPI;
       uint8_t* dst = stage + (l >> 2) * (N * 128) + row * 128 + (LO ? (D / 64) * (N * 128) : 0);
       const int c0 = 2 * (l & 3), odd = D > 64 ? (l >> 2) & 1 : 0;
@@ -482,118 +608,210 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       *(uint4*)(dst + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? v1 : v0;
       *(uint4*)(dst + (((c0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? v0 : v1;
     };
+    // ... times the norm of the row (mul: this lane's row's, two halves hi + lo for K)
+    auto scale_row = [&](auto IV, uint32_t (&h)[8], uint32_t mul, int i) {
+      constexpr bool V = decltype(IV)::value;
+      const uint32_t m = __shfl_sync(0xffffffffu, mul, i * C::RPI + rsub);
+      const uint32_t a = __byte_perm(m, 0, 0x1010), b = __byte_perm(m, 0, 0x3232);
+      const __half2 hi = *(const __half2*)&a, lo = *(const __half2*)&b;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __half2 c = *(const __half2*)&h[j];
+        const __half2 x = V ? __hmul2(c, hi) : __hfma2(c, hi, __hmul2(c, lo));
+        h[j] = *(const uint32_t*)&x;
+      }
+    };
     using KI = std::false_type;
     using VI = std::true_type;
     // norms of row w N / 4 + lane, one tile ahead
-    const int nrow = w * (N / 4) + lane;
+    const int nrow = w * (N / kDequantWarps) + lane;
     float nk = 0.f, nv = 0.f;
     int first = -1;
-    auto load_norms = [&](int k, const Bases& from) {
+    auto load_norms = [&](int k, const Pages& from) {
       nk = nv = 0.f;
       first = -1;
-      const uint8_t* pg = from.at[WP > 1 ? lane / kBlockSize : 0];
-      if (lane < N / 4 && pg != nullptr) {
+      const uint8_t* pg = base_of(from.id[WP > 1 ? lane / kBlockSize : 0]);
+      if (lane < N / kDequantWarps && pg != nullptr) {
         first = span.at((k_begin + k) * C::PPT + nrow / kBlockSize) * kBlockSize;
         const uint8_t* sl = pg + (nrow % kBlockSize) * p.row_stride;
         nk = *(const float*)(sl + KPACK);
         nv = *(const float*)(sl + p.k_region + VPACK);
       }
     };
-    auto store_norms = [&](int k) {
-      const int buf = k & 1;
+    // Norms and facts of tile k for the softmax warps; kmul, vmul: the factors of this lane's
+    // row in the operands (halves hi and lo; 1 and 0 where the softmax applies the norms).
+    uint32_t kmul = 0x00003c00u, vmul = 0x00003c00u;
+    auto publish = [&](int k) {
+      const int buf = k & nmask, mb = k & 1;
       bool ok = true;
-      float hi = -100.0f, lo = 1e30f;
-      if (lane < N / 4) {
-        norm_s[buf * 2 * N + nrow] = nk;
-        norm_s[buf * 2 * N + N + nrow] = nv;
+      int kmax = -100, kmin = 1000, vmax = -100, vmin = 1000;
+      if (lane < N / kDequantWarps) {
+        norms[buf * 2 * N + nrow] = nk;
+        norms[buf * 2 * N + N + nrow] = nv;
         if (nrow % kBlockSize == 0) ms->tok[buf][nrow / kBlockSize] = first;
         const int tok = first + nrow % kBlockSize;
         ok = first >= 0 && tok <= pos_first && (tok >= low_last || tok < p.sinks) && isfinite(nk) &&
              isfinite(nv);
-        hi = fmaxf(log2_bound(nv), -100.0f);
-        if (nv != 0.f) lo = fmaxf(log2_bound(fabsf(nv)), -100.0f);
+        kmax = (int)ceilf(fmaxf(log2_bound(fabsf(nk)), -100.0f));
+        vmax = (int)ceilf(fmaxf(log2_bound(fabsf(nv)), -100.0f));
+        if (nk != 0.f) kmin = kmax;
+        if (nv != 0.f) vmin = vmax;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      }
+      kmax = __reduce_max_sync(0xffffffffu, kmax);
+      kmin = __reduce_min_sync(0xffffffffu, kmin);
+      vmax = __reduce_max_sync(0xffffffffu, vmax);
+      vmin = __reduce_min_sync(0xffffffffu, vmin);
       ok = __all_sync(0xffffffffu, ok);
-      if (lane == 0) ms->meta[buf][w] = TileMeta{hi, lo, ok ? 1 : 0};
+      if (lane == 0) ms->meta[mb][w] = TileMeta{kmax, kmin, vmax, vmin, ok ? 1 : 0};
+      asm volatile("bar.sync 1, 128;" ::: "memory");     // the dequantizing warps
+#pragma unroll
+      for (int i = 0; i < kDequantWarps; ++i) {
+        const TileMeta m = ms->meta[mb][i];
+        ok = ok && m.plain;
+        kmax = max(kmax, m.kmax);
+        kmin = min(kmin, m.kmin);
+        vmax = max(vmax, m.vmax);
+        vmin = min(vmin, m.vmin);
+      }
+      ok = ok && vmax - vmin <= 8 && abs(vmax) < 60;
+      float ks = 1.0f;
+      if constexpr (!PREC) {
+        ok = ok && kmax - kmin <= 8 && abs(kmax) < 60;
+        kmul = vmul = 0x00003c00u;
+        if (ok) {
+          const float sk = nk * __int_as_float((127 - kmax) << 23);
+          const float hi = __half2float(__float2half_rn(sk));
+          kmul = pack_half2(hi, sk - hi);
+          vmul = pack_half2(nv * __int_as_float((127 - vmax) << 23), 0.f);
+          ks = __int_as_float((127 + kmax) << 23);
+        }
+      }
+      if (w == 0 && lane == 0) ms->info[buf] = TileInfo{ok ? 1 : 0, ks, (float)vmax};
       __syncwarp();
-      mbar_arrive(&ms->norm_full[buf]);
+      if (lane == 0) mbar_arrive(&ms->norm_full[buf]);
     };
     auto free_stage = [&](int at) {                      // wait until ring position `at` may be written
       return at < C::RING ||
-             mbar_wait(&ms->ring_empty[at % C::RING], (uint32_t)(at / C::RING - 1) & 1u, p.wait_ms);
+             tile_wait(&ms->ring_empty[at % C::RING], (uint32_t)(at / C::RING - 1) & 1u, p.wait_ms);
     };
-    auto load_all = [&](auto IV, const Bases& from) {
+    auto load_all = [&](auto IV, auto& raw, const Pages& from) {
       const uint8_t* at = nullptr;
 #pragma unroll
-      for (int i = 0; i < C::IT; ++i) load_rows(IV, raw[i], i, from, at);
+      for (int i = 0; i < C::IT; ++i) load_rows(IV, raw, i, from, at);
     };
-    // the codes in raw to ring position pos; as each is used its register takes the codes of
-    // the next unit (kind INV, from these pages)
-    auto produce = [&](auto IV, auto INV, int pos, bool more, const Bases& next) {
+    // The codes in raw to ring position pos, some rows' lookups in flight; as each is used its
+    // registers take the codes of a coming unit (kind INV, from these pages).
+    auto produce = [&](auto IV, auto& raw, auto INV, auto& coming, int pos, uint32_t mul, bool more,
+                       const Pages& next) {
+      constexpr bool V = decltype(IV)::value;
       uint8_t* stage = ring_s + (pos % C::RING) * C::STAGE;
       const uint8_t* at = nullptr;
+      constexpr int U = C::IT % 4 == 0 ? 4 : C::IT % 2 == 0 ? 2 : 1;   // rows in flight
 #pragma unroll
-      for (int i = 0; i < C::IT; ++i) {
-        store_one(IV, std::false_type{}, raw[i], i, stage);
-        if constexpr (C::kKeyLo && !decltype(IV)::value) store_one(IV, std::true_type{}, raw[i], i, stage);
-        if (more) load_rows(INV, raw[i], i, next, at);
+      for (int i = 0; i < C::IT; i += U) {
+        uint32_t h[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) look_up(IV, std::false_type{}, raw, i + u, h[u]);
+        if constexpr (!PREC) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) scale_row(IV, h[u], mul, i + u);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) store_row(std::false_type{}, h[u], i + u, stage);
+        if constexpr (C::kKeyLo && !V) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) look_up(IV, std::true_type{}, raw, i + u, h[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) store_row(std::true_type{}, h[u], i + u, stage);
+        }
+        if (more) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) load_rows(INV, coming, i + u, next, at);
+        }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&ms->ring_full[pos % C::RING]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->ring_full[pos % C::RING]);
     };
+    constexpr int RW = C::KW > C::VW ? C::KW : C::VW;
+    uint32_t raw_k[C::IT][C::kDeep ? C::KW : RW];
+    uint32_t raw_x[C::IT][C::kDeep ? C::VW : 1];
+    auto& raw_v = [&]() -> auto& {
+      if constexpr (C::kDeep) return raw_x;
+      else return raw_k;
+    }();
     bool ok = true;
     if (tiles > 0) {
-      Bases bk = fetch(0), bv = bk;                      // of the latest K tile, of the next V tile
-      load_norms(0, bk);
-      load_all(KI{}, bk);
+      // pages of tiles k, k + 1, k + 2 (as far as they are needed)
+      Pages b0 = fetch(0), b1 = b0, b2 = b0;
+      load_norms(0, b0);
+      load_all(KI{}, raw_k, b0);
+      if constexpr (C::kDeep) load_all(VI{}, raw_v, b0);
       if (two) {                                         // K(0), V(0), K(1), V(1), ...
         for (int k = 0; k < tiles; ++k) {
+          const bool more = k + 1 < tiles;
+          // the norms' buffer: item k - 2 of both slots is past its P V when V(k - 2)'s stage,
+          // which K(k) takes, is free
           ok = free_stage(k_at(k));
           if (!ok) break;
-          store_norms(k);
-          produce(KI{}, VI{}, k_at(k), true, bk);
-          const bool more = k + 1 < tiles;
+          publish(k);
           if (more) {
-            bk = fetch(k + 1);
-            load_norms(k + 1, bk);
+            b1 = fetch(k + 1);
+            load_norms(k + 1, b1);
           }
+          if constexpr (C::kDeep) produce(KI{}, raw_k, KI{}, raw_k, k_at(k), kmul, more, b1);
+          else produce(KI{}, raw_k, VI{}, raw_v, k_at(k), kmul, true, b0);
           ok = free_stage(v_at(k));
           if (!ok) break;
-          produce(VI{}, KI{}, v_at(k), more, bk);
+          if constexpr (C::kDeep) produce(VI{}, raw_v, VI{}, raw_v, v_at(k), vmul, more, b1);
+          else produce(VI{}, raw_v, KI{}, raw_k, v_at(k), vmul, more, b1);
+          b0 = b1;
         }
       } else {                                           // K(0), K(1), V(0), K(2), V(1), ...
-        store_norms(0);
+        publish(0);
+        uint32_t vmul_now = vmul;
         if (tiles > 1) {
-          bk = fetch(1);
-          load_norms(1, bk);
+          b1 = fetch(1);
+          load_norms(1, b1);
         }
-        produce(KI{}, KI{}, k_at(0), tiles > 1, bk);
-        if (tiles == 1) load_all(VI{}, bv);
+        produce(KI{}, raw_k, KI{}, raw_k, k_at(0), kmul, tiles > 1, b1);
+        if (!C::kDeep && tiles == 1) load_all(VI{}, raw_v, b0);
         for (int k = 0; k < tiles; ++k) {
-          if (k + 1 < tiles) {
+          vmul_now = vmul;
+          const bool more1 = k + 1 < tiles, more2 = k + 2 < tiles;
+          if (more2) b2 = fetch(k + 2);
+          if (more1) {
             ok = free_stage(k_at(k + 1));
             if (!ok) break;
-            produce(KI{}, VI{}, k_at(k + 1), true, bv);
-            // the norms' buffer is free once item k - 1 has its weights
-            if (k >= 1) ok = mbar_wait(&ms->p_ready[(k - 1) & 1], (uint32_t)((k - 1) >> 1) & 1u, p.wait_ms);
-            if (!ok) break;
-            store_norms(k + 1);
-          }
-          bv = bk;
-          const bool more = k + 2 < tiles;
-          if (more) {
-            bk = fetch(k + 2);
-            load_norms(k + 2, bk);
+            if constexpr (!PREC) {
+              // the norms' buffer: item k - 3 is past its P V (its V's stage was K(k)'s)
+              publish(k + 1);
+              if (more2) load_norms(k + 2, b2);
+            }
+            if constexpr (C::kDeep) produce(KI{}, raw_k, KI{}, raw_k, k_at(k + 1), kmul, more2, b2);
+            else produce(KI{}, raw_k, VI{}, raw_v, k_at(k + 1), kmul, true, b0);
+            if constexpr (PREC) {
+              // the norms' buffer is free once the last item of tile k - 1 has its weights
+              if (k >= 1) {
+                const int j = C::kOneO ? 0 : (k - 1) & 1;
+                const int m = (C::kOneO ? k - 1 : (k - 1) >> 1) * C::H + C::H - 1;
+                ok = tile_wait(&ms->p_ready[j][m & 1], (uint32_t)(m >> 1) & 1u, p.wait_ms);
+              }
+              if (!ok) break;
+              publish(k + 1);
+              if (more2) load_norms(k + 2, b2);
+            }
           }
           ok = free_stage(v_at(k));
           if (!ok) break;
-          produce(VI{}, KI{}, v_at(k), more, bk);
-          if (k + 2 == tiles) load_all(VI{}, bv);        // no K tile is left to fetch it under
+          if constexpr (C::kDeep) {
+            produce(VI{}, raw_v, VI{}, raw_v, v_at(k), vmul_now, more1, b1);
+          } else {
+            produce(VI{}, raw_v, KI{}, raw_k, v_at(k), vmul_now, more2, b2);
+            if (more1 && !more2) load_all(VI{}, raw_v, b1);   // no K tile is left to fetch it under
+          }
+          b0 = b1;
+          b1 = b2;
         }
       }
     }
@@ -606,55 +824,74 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     float M = -INFINITY, sum = 0.f;
     const int pos = myrow < rows ? p0 + (r0 + myrow) / G : -1;
     const int low = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
-    const uint32_t o_at = tmem + lanes + O_COL + (C::kOneO ? 0 : slot * D);
-    const int step_n = C::kOneO ? 1 : 2;
-    bool ok = true, any = false;
-    for (int n = slot; n < items && !(C::kOneO && slot); n += step_n) {
-      const int buf = n & 1, k = two ? n >> 1 : n, nb = k & 1;
-      const uint32_t s_at = tmem + lanes + S_COL + buf * 128;
-      ok = mbar_wait(&ms->norm_full[nb], (uint32_t)(k >> 1) & 1u, p.wait_ms) &&
-           mbar_wait(&ms->s_full[buf], (uint32_t)(n >> 1) & 1u, p.wait_ms);
+    const uint32_t o_at = tmem + lanes + slot * D;
+    const int items = slot_tiles(slot) * C::H;
+    bool ok = true;
+    for (int n = 0; n < items; ++n) {
+      const int k = slot_tile(slot, n / C::H), nb = k & nmask, half = n % C::H;
+      const uint32_t s_at = tmem + lanes + 256 + slot * 128 + (n & 1) * 64;
+      ok = (half || tile_wait(&ms->norm_full[nb], (uint32_t)(k >> nshift) & 1u, p.wait_ms)) &&
+           tile_wait(&ms->s_full[slot][n & 1], (uint32_t)(n >> 1) & 1u, p.wait_ms);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      float s[N];
-#pragma unroll
-      for (int c = 0; c < N; c += 16) tmem_ld16_nowait(s_at + c, s + c);
-      const float* nks = norm_s + nb * 2 * N;
+      float s[NI];
+      const float* nks = norms + nb * 2 * N + half * NI;
       const float* nvs = nks + N;
-      bool plain = true;
-      float emax = -100.f, emin = 1e30f;
+      const TileInfo info = ms->info[nb];
+      const bool plain = info.plain;
+      const float qt = qs * info.ek_scale;
+      // x of 16 columns at c, key by key: norms and masks here (a tile that is not plain)
+      auto masked = [&](int c, float (&x)[16]) {
+        tmem_ld16_nowait(s_at + c, x);
+        const int first = ms->tok[nb][(half * NI + c) / kBlockSize];
+        tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const TileMeta m = ms->meta[nb][i];
-        plain = plain && m.plain;
-        emax = fmaxf(emax, m.emax);
-        emin = fminf(emin, m.emin);
-      }
-      plain = plain && emax - emin <= 8.0f;
-      tmem_wait_ld();
+        for (int i = 0; i < 16; ++i) {
+          const int tok = first + i;
+          const bool see = first >= 0 && tok <= pos && (tok >= low || tok < p.sinks);
+          x[i] = see ? x[i] * nks[c + i] * qs : -INFINITY;
+        }
+      };
       float z = -INFINITY;
       if (plain) {
-        float z1 = -INFINITY;
+        // the first half's maxima while the second half is read
+        constexpr int HL = NI >= 32 ? NI / 2 : NI;
+        float zz[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < N; c += 4) {
-          const float4 f = *(const float4*)(nks + c);
-          float2 u = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
-          float2 v = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
-          s[c] = u.x, s[c + 1] = u.y, s[c + 2] = v.x, s[c + 3] = v.y;
-          z = fmaxf(z, fmaxf(u.x, u.y));
-          z1 = fmaxf(z1, fmaxf(v.x, v.y));
+        for (int c = 0; c < HL; c += 16) tmem_ld16_nowait(s_at + c, s + c);
+#pragma unroll
+        for (int h = 0; h < NI; h += HL) {
+          tmem_wait_ld();
+          if (h + HL < NI) {
+#pragma unroll
+            for (int c = h + HL; c < h + 2 * HL; c += 16) tmem_ld16_nowait(s_at + c, s + c);
+          }
+#pragma unroll
+          for (int c = h; c < h + HL; c += 8) {
+            if constexpr (PREC) {
+#pragma unroll
+              for (int i = c; i < c + 8; i += 4) {
+                const float4 f = *(const float4*)(nks + i);
+                const float2 u = mul2(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
+                const float2 v = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
+                s[i] = u.x, s[i + 1] = u.y, s[i + 2] = v.x, s[i + 3] = v.y;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) zz[j] = max3(zz[j], s[c + 2 * j], s[c + 2 * j + 1]);
+          }
         }
-        z = fmaf(fmaxf(z, z1), qs, emax);
+        z = fmaf(max3(fmaxf(zz[0], zz[1]), zz[2], zz[3]), qt, info.ev);
       } else {
+#pragma unroll 1
+        for (int c = 0; c < NI; c += 16) {
+          float x[16];
+          masked(c, x);
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const int first = ms->tok[nb][c / kBlockSize], tok = first + c % kBlockSize;
-          const bool see = first >= 0 && tok <= pos && (tok >= low || tok < p.sinks);
-          s[c] = see ? s[c] * nks[c] * qs : -INFINITY;
-          z = fmaxf(z, s[c] + fmaxf(log2_bound(nvs[c]), -100.0f));
+          for (int i = 0; i < 16; ++i) z = fmaxf(z, x[i] + fmaxf(log2_bound(nvs[c + i]), -100.0f));
         }
       }
       const bool raise = z > M + kLazyRescale;
@@ -663,16 +900,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         const float f = M == -INFINITY ? 0.f : exp2f(M - to);
         sum *= f;
         M = to;
-        if (any) {
-          // With a slot's own O', P V of its last item precedes Q K of this one.  A shared O'
-          // may still be under P V of item n - 1: until that has freed its V tile.
-          if constexpr (C::kOneO) {
-            const int at = v_at(n - 1);
-            ok = mbar_wait(&ms->ring_empty[at % C::RING], (uint32_t)(at / C::RING) & 1u, p.wait_ms);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-          }
+        if (n > 0) {                                     // until P V of the last item is done
+          ok = tile_wait(&ms->pv_done[slot], (uint32_t)(n - 1) & 1u, p.wait_ms);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -685,43 +917,60 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
           }
         }
       }
-      any = true;
       const float ref = M == -INFINITY ? 0.f : M;
       uint32_t pk[8];
       if (plain) {
-        const float2 q2 = make_float2(qs, qs), m2 = make_float2(-ref, -ref);
-        float2 l0 = make_float2(sum, 0.f), l1 = make_float2(0.f, 0.f);
+        // without PREC: P = 2^(x + ev - M), the norms (over 2^ev) are in the operands
+        const float shift = PREC ? -ref : info.ev - ref;
+        const float2 q2 = make_float2(qt, qt), m2 = make_float2(shift, shift);
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0, l2 = l0, l3 = l0;
 #pragma unroll
-        for (int c = 0; c < N; c += 4) {
-          float2 u = fma2(make_float2(s[c], s[c + 1]), q2, m2);
-          float2 v = fma2(make_float2(s[c + 2], s[c + 3]), q2, m2);
-          u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-          v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-          l0 = add2(l0, u);
-          l1 = add2(l1, v);
-          const float4 f = *(const float4*)(nvs + c);
-          u = mul2(u, make_float2(f.x, f.y));
-          v = mul2(v, make_float2(f.z, f.w));
-          pk[c / 2 % 8] = pack_half2(u.x, u.y);
-          pk[c / 2 % 8 + 1] = pack_half2(v.x, v.y);
-          if (c % 16 == 12) tmem_st8(s_at + c / 16 * 8, pk);
+        for (int c = 0; c < NI; c += 8) {
+          float2 u[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = fma2(make_float2(s[c + 2 * j], s[c + 2 * j + 1]), q2, m2);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = make_float2(ex2_approx(u[j].x), ex2_approx(u[j].y));
+          l0 = add2(l0, u[0]);
+          l1 = add2(l1, u[1]);
+          l2 = add2(l2, u[2]);
+          l3 = add2(l3, u[3]);
+          if constexpr (PREC) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const float4 f = *(const float4*)(nvs + c + 2 * j);
+              u[j] = mul2(u[j], make_float2(f.x, f.y));
+              u[j + 1] = mul2(u[j + 1], make_float2(f.z, f.w));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pk[c / 2 % 8 + j] = pack_half2(u[j].x, u[j].y);
+          if (c % 16 == 8) tmem_st8(s_at + c / 16 * 8, pk);
         }
-        sum = (l0.x + l0.y) + (l1.x + l1.y);
+        l0 = add2(add2(l0, l1), add2(l2, l3));
+        const float part = l0.x + l0.y;
+        sum = PREC ? sum + part : fmaf(part, __int_as_float((127 - (int)info.ev) << 23), sum);
       } else {
+#pragma unroll 1
+        for (int c = 0; c < NI; c += 16) {                // P of a chunk lies over scores already read
+          float x[16];
+          masked(c, x);
 #pragma unroll
-        for (int c = 0; c < N; c += 2) {
-          const float w0 = ex2_approx(s[c] - ref), w1 = ex2_approx(s[c + 1] - ref);
-          sum += w0 + w1;
-          pk[c / 2 % 8] = pack_half2(s[c] == -INFINITY ? 0.f : w0 * nvs[c],
-                                     s[c + 1] == -INFINITY ? 0.f : w1 * nvs[c + 1]);
-          if (c % 16 == 14) tmem_st8(s_at + c / 16 * 8, pk);
+          for (int i = 0; i < 16; i += 2) {
+            const float w0 = ex2_approx(x[i] - ref), w1 = ex2_approx(x[i + 1] - ref);
+            sum += w0 + w1;
+            pk[i / 2] = pack_half2(x[i] == -INFINITY ? 0.f : w0 * nvs[c + i],
+                                   x[i + 1] == -INFINITY ? 0.f : w1 * nvs[c + i + 1]);
+          }
+          tmem_st8(s_at + c / 2, pk);
         }
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&ms->p_ready[buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->p_ready[slot][n & 1]);
     }
-    if (ok && items > 0) ok = mbar_wait(&ms->o_done, 0, p.wait_ms);
+    if (ok && tiles > 0) ok = tile_wait(&ms->o_done, 0, p.wait_ms);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) fail();
     // every other reader of the operands is done: their place takes the partials
@@ -731,7 +980,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         float o[16];
-        if (any && ok) {
+        if (items > 0 && ok) {
           tmem_ld16_nowait(o_at + c, o);
           tmem_wait_ld();
         } else {
@@ -753,30 +1002,48 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   if (ctas > 1) cluster.sync();
   // row r is joined by CTA r % ctas of the cluster, by a warp; records: CTAs x slots
   const int recs = two || C::kOneO ? 1 : 2;
-  for (int r = split + ctas * warp; r < rows; r += ctas * 16) {
-    float Mr = -INFINITY, lr = 0.f, o[E];
+  constexpr int RB = 2;                   // rows of a warp at once
+  uint32_t sgn[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = 0.f;
-    fold_records<E>(ctas * recs, [&](int j, float& m, float& ll, float (&v)[E]) {
-      const float* from = part_s + ((recs == 2 ? (j & 1) * kTileRows : 0) + r) * PART;
-      if (ctas > 1) from = cluster.map_shared_rank(from, recs == 2 ? j >> 1 : j);
-      m = from[D];
-      ll = from[D + 1];
+  for (int i = 0; i < E; ++i) sgn[i] = sign_mask_at(p.sign_seed, lane * E + i);
+  for (int rb = split + ctas * warp; rb < rows; rb += ctas * kTilesWarps * RB) {
+    float Mr[RB], lr[RB], o[RB][E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = from[lane * E + i];
-    }, Mr, lr, o);
-    const float inv = lr == 0.f ? 0.f : 1.0f / (lr * av);     // a row that sees nothing: 0
+    for (int j = 0; j < RB; ++j) {
+      Mr[j] = -INFINITY;
+      lr[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] *= inv;
-    warp_fwht<E>(o, lane);
-    const int rr = r0 + r;
-    const int64_t off = (int64_t)(sq.row0 + rr / G) * p.o_rstride +
-                        (int64_t)(kvh * G + rr % G) * p.o_hstride + lane * E;
+      for (int i = 0; i < E; ++i) o[j][i] = 0.f;
+      const int r = rb + j * ctas * kTilesWarps;
+      if (r >= rows) continue;
+      auto record = [&](int i, float& m, float& ll, float (&v)[E]) {
+        const float* from = part_s + ((recs == 2 ? (i & 1) * kTileRows : 0) + r) * PART;
+        if (ctas > 1) from = cluster.map_shared_rank(from, recs == 2 ? i >> 1 : i);
+        m = from[D];
+        ll = from[D + 1];
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      store_from_f32(p.out, off + i, p.out_dtype,
-                     __uint_as_float(__float_as_uint(o[i] * inv_sqrt_dim<D>()) ^
-                                     sign_mask_at(p.sign_seed, lane * E + i)));
+        for (int e = 0; e < E; ++e) v[e] = from[lane * E + e];
+      };
+      if (ctas * recs == 1) record(0, Mr[j], lr[j], o[j]);
+      else fold_records<E>(ctas * recs, record, Mr[j], lr[j], o[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const float inv = lr[j] == 0.f ? 0.f : 1.0f / (lr[j] * av);   // a row that sees nothing: 0
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[j][i] *= inv * inv_sqrt_dim<D>();
+      warp_fwht<E>(o[j], lane);
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[j][i] = __uint_as_float(__float_as_uint(o[j][i]) ^ sgn[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const int r = rb + j * ctas * kTilesWarps, rr = r0 + r;
+      if (r >= rows) continue;
+      const int64_t off = (int64_t)(sq.row0 + rr / G) * p.o_rstride +
+                          (int64_t)(kvh * G + rr % G) * p.o_hstride + lane * E;
+      store_run<E>(o[j], p.out, off, p.out_dtype, p.out_vec);
+    }
   }
   if (ctas > 1) cluster.sync();              // no CTA leaves while its partials may be read
 }
