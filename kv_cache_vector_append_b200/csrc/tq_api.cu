@@ -639,13 +639,12 @@ tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* 
   p.o_rstride = out.stride[0];
   p.o_hstride = out.stride[1];
   p.out_dtype = out.dtype;
-  auto runs_aligned = [&](const tq_tensor& t) {
-    const int64_t run = D / 32 * dtype_size(t.dtype), a = run < 16 ? run : 16;
-    return (uintptr_t)t.data % a == 0 && t.stride[0] * dtype_size(t.dtype) % a == 0 &&
-           t.stride[1] * dtype_size(t.dtype) % a == 0;
+  auto rows_aligned = [](const tq_tensor& t) {
+    const int64_t size = dtype_size(t.dtype);
+    return (uintptr_t)t.data % 16 == 0 && t.stride[0] * size % 16 == 0 && t.stride[1] * size % 16 == 0;
   };
-  p.q_vec = runs_aligned(q);
-  p.out_vec = runs_aligned(out);
+  p.q_vec = rows_aligned(q);
+  p.out_vec = rows_aligned(out);
   p.group = (int32_t)group;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.sign_seed = sign_seed;

@@ -32,7 +32,7 @@ struct AttendParams {
   void* out;
   int64_t o_rstride, o_hstride;
   int32_t out_dtype;
-  bool q_vec, out_vec;          // runs of D / 32 elements are aligned to their size (16 at most)
+  bool q_vec, out_vec;          // rows start on 16-byte boundaries
   int32_t group;
   float scale_log2;             // softmax scale * log2(e)
   uint64_t sign_seed;

@@ -39,10 +39,10 @@ tq_status launch_rows_t(const AttendParams& p, const DeviceInfo& di, cudaStream_
   return launch_status();
 }
 
-template <int D, int KB, int VB, bool PREC>
+template <int D, int KB, int VB>
 tq_status launch_tiles_t(AttendParams p, const DeviceInfo& di, cudaStream_t st) {
-  using C = TilesCfg<D, KB, VB, PREC>;
-  auto kern = attend_tiles_kernel<D, KB, VB, PREC>;
+  using C = TilesCfg<D, KB, VB>;
+  auto kern = attend_tiles_kernel<D, KB, VB>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return TQ_ERR_CUDA;
   // the split of registers between the warpgroups counts on the launch's own number
@@ -90,18 +90,13 @@ tq_status launch_rows_kbits(int vb, const AttendParams& p, const DeviceInfo& di,
   }
 }
 
-template <int D, int KB, int VB>
-tq_status launch_tiles_out(const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
-  if (p.out_dtype == TQ_BF16) return launch_tiles_t<D, KB, VB, false>(p, di, st);
-  return launch_tiles_t<D, KB, VB, true>(p, di, st);
-}
 template <int D, int KB>
 tq_status launch_tiles_kbits(int vb, const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
   switch (vb) {
-    case 2: return launch_tiles_out<D, KB, 2>(p, di, st);
-    case 3: return launch_tiles_out<D, KB, 3>(p, di, st);
-    case 4: return launch_tiles_out<D, KB, 4>(p, di, st);
-    case 8: return launch_tiles_out<D, KB, 8>(p, di, st);
+    case 2: return launch_tiles_t<D, KB, 2>(p, di, st);
+    case 3: return launch_tiles_t<D, KB, 3>(p, di, st);
+    case 4: return launch_tiles_t<D, KB, 4>(p, di, st);
+    case 8: return launch_tiles_t<D, KB, 8>(p, di, st);
     default: return TQ_ERR_UNSUPPORTED;
   }
 }

@@ -2,19 +2,19 @@
 // new tokens), on the tcgen05 tensor cores.
 //
 // Math.  As in tq_attend_rows.cuh, in the rotated domain: S = q^ C~^T on the codes' centroids,
-// x = S nK |q'| scale log2(e) per (row, key), P = 2^(x - M) nV in fp16, O' += P V~,
-// o = R^T O' / l.  Norms never enter an operand, so keys and values keep the precision of
-// their centroids; statistics and accumulators are fp32.  The centroids are scaled by a factor
-// in [1, 2) under which their fp16 roundings are smallest (a search over 512 factors; exact to
-// about 2^-13 of the largest), which leaves with the scales of the rows.
-//   PREC (out is f16 or f32): q^ = hi + lo (two fp16), and 8-bit keys too, so that scores are
-//   right to about 2^-20; bf16 outputs take the fp16 operands alone (2^-12).
+// x = S nK |q'| scale log2(e) per (row, key), P = 2^(x - M), O' += P V~, o = R^T O' / l;
+// statistics and accumulators are fp32.  fp16 operands: unit queries (2^-12 off, as their sum
+// over coordinates of either sign), centroids of keys times a factor in [1, 2) under which their
+// roundings are smallest (a search over 512 factors; it leaves with the rows' scales), values
+// c nV 2^-ev, P.  Together about 6e-4 of the output, a third of bf16's own rounding.  Key norms
+// stay out of the operand: in it they would be rounded key by key, which costs 1e-3.
 // M >= max(x + log2 nV): a tile whose V norms lie within 2^8 of each other and which every row
-// sees takes the tile's largest norm for all of them, any other the bound key by key, masks
-// included: what a row does not see never touches it.
+// sees takes the power 2^ev above its largest norm for all of them; in any other tile V~ = c,
+// P = 2^(x - M) nV, and the bound goes key by key, masks included, so that what a row does not
+// see never touches it.
 //
 // Layout.  A CTA holds two slots of 128 rows x N keys: two row tiles that share every key tile
-// (256 rows), or, with 128 rows or in PREC, one row tile whose key tiles alternate between the
+// (256 rows), or, with 128 rows, one row tile whose key tiles alternate between the
 // slots, each with its own (M, l, O'), joined at the end.  (D = 256: one O' fills the tensor
 // memory; one softmax warpgroup, two score buffers.)  Warps 0-7 are the slots' softmax
 // warpgroups (a thread = a row: scores from tensor memory, P back over them), warps 8-11 turn
@@ -44,31 +44,26 @@ constexpr int kTilesMaxCtas = 8;
 constexpr int kTilesRegs = 128, kSoftmaxRegs = 152, kDequantRegs = 128, kIssueRegs = 80;
 static_assert(2 * kSoftmaxRegs + kDequantRegs + kIssueRegs <= 4 * kTilesRegs, "registers of a CTA");
 
-template <int D, int KB, int VB, bool PREC>
+template <int D, int KB, int VB>
 struct TilesCfg {
-  static constexpr bool kTwoTiles = !PREC && D <= 128;   // may hold two row tiles
+  static constexpr bool kTwoTiles = D <= 128;            // may hold two row tiles
   static constexpr bool kOneO = D == 256;                // one accumulator, one softmax warpgroup
-  static constexpr bool kKeyLo = PREC && KB == 8;
-  static constexpr int QPARTS = PREC ? 2 : 1;
-  static constexpr int KPARTS = kKeyLo ? 2 : 1;
   // bytes of a ring stage, keys of a tile
-  static constexpr int STAGE = D == 64 ? 16384 * KPARTS : (D == 256 && PREC ? 16384 : 32768);
-  static constexpr int N = STAGE / (2 * D * KPARTS);
-  static constexpr int RING = D == 256 && PREC ? 2 : 3;
+  static constexpr int STAGE = D == 64 ? 16384 : 32768, N = STAGE / (2 * D), RING = 3;
   static constexpr int PPT = N / kBlockSize;             // pages a tile
   // A slot works on items of NI keys of a tile, two score buffers in turn
   static constexpr int NI = N < 64 ? N : 64, H = N / NI;
-  static constexpr int QTILE = kTileRows * D * 2;        // one part of one row tile
-  static constexpr int QBYTES = (kTwoTiles ? 2 : 1) * QPARTS * QTILE;
+  static constexpr int QTILE = kTileRows * D * 2;
+  static constexpr int QBYTES = (kTwoTiles ? 2 : 1) * QTILE;
   static constexpr int PART = D + 4;                     // floats of a row's partial
   static constexpr int STAGING = (kOneO ? 1 : 2) * kTileRows * PART * 4;
   static constexpr int OPER = QBYTES + RING * STAGE > STAGING ? QBYTES + RING * STAGE : STAGING;
   static constexpr int LUT = kLutRow * (lut_entries(KB) > lut_entries(VB) ? lut_entries(KB) : lut_entries(VB));
   // norms [buffer][K, V][N]; a row tile whose key tiles alternate uses four buffers, at D <= 128
-  // without PREC in the place of the second row tile's q
-  static constexpr int NBUF = PREC || !kOneO ? 2 : 4;
+  // in the place of the second row tile's q
+  static constexpr int NBUF = kOneO ? 4 : 2;
   static constexpr int NORMS = NBUF * N * 2 * 4;
-  static constexpr int MISC = 896;
+  static constexpr int MISC = 640;
   // more than half an SM: a CTA that holds all of tensor memory has the SM to itself
   static constexpr int RAW = OPER + LUT + NORMS + MISC;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
@@ -81,28 +76,28 @@ struct TilesCfg {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// What the dequantizing warps know of their N / 4 keys of a tile: bounds of log2 of the norms,
-// and whether every row of the CTA sees every key and all norms are finite.
+// What the dequantizing warps know of their N / 4 keys of a tile: bounds of log2 nV, and whether
+// every row of the CTA sees every key and all norms are finite.
 struct TileMeta {
-  int kmax, kmin, vmax, vmin, plain;
+  int vmax, vmin, plain;
 };
-// And of the whole tile.  plain: no masks, V norms within 2^8 of each other; without PREC also
-// K norms, and the operands then hold nK 2^-ek c and nV 2^-ev c, else c alone.
+// And of the whole tile.  plain: no masks, V norms within 2^8 of each other; the operand then
+// holds c nV 2^-ev, else c alone.
 struct TileInfo {
   int plain;
-  float ek_scale;                          // 2^ek
   float ev;
 };
 
 struct TilesMisc {
-  uint64_t s_full[2][2], p_ready[2][2], pv_done[2], norm_full[4], ring_full[3], ring_empty[3], o_done;
-  unsigned long long best[2];
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2], norm_full[4], ring_full[3], ring_empty[3], o_done, q_ready;
+  unsigned long long best;
+  float alpha;
   uint32_t tmem;
   int tok[4][8];                           // first token of a page of the tile; < 0: no page
   TileMeta meta[2][kDequantWarps];
   TileInfo info[4];
 };
-static_assert(sizeof(TilesMisc) <= 896, "misc area");
+static_assert(sizeof(TilesMisc) <= 640, "misc area");
 
 __device__ __forceinline__ void umma_ts_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -196,64 +191,14 @@ struct Codes16 {
   }
 };
 
-// E consecutive elements at element off; vec: the run is aligned to its size (16 bytes at most).
-template <int E>
-__device__ __forceinline__ void load_run(float (&x)[E], const void* base, int64_t off, int32_t dtype, bool vec) {
-  if (vec && dtype != TQ_F32) {
-    uint32_t w[E / 2];
-    const uint32_t* a = (const uint32_t*)((const uint16_t*)base + off);
-    if constexpr (E == 2) w[0] = *a;
-    else if constexpr (E == 4) *(uint2*)w = *(const uint2*)a;
-    else *(uint4*)w = *(const uint4*)a;
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      if (dtype == TQ_BF16) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(*(const __half2*)&w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = load_as_f32(base, off + i, dtype);
-  }
-}
-template <int E>
-__device__ __forceinline__ void store_run(const float (&x)[E], void* base, int64_t off, int32_t dtype, bool vec) {
-  if (vec && dtype != TQ_F32) {
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      if (dtype == TQ_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *(const uint32_t*)&h;
-      } else {
-        w[i] = pack_half2(x[2 * i], x[2 * i + 1]);
-      }
-    }
-    uint32_t* a = (uint32_t*)((uint16_t*)base + off);
-    if constexpr (E == 2) *a = w[0];
-    else if constexpr (E == 4) *(uint2*)a = *(const uint2*)w;
-    else *(uint4*)a = *(const uint4*)w;
-  } else if (vec) {
-#pragma unroll
-    for (int i = 0; i < E; i += 2) *(float2*)((float*)base + off + i) = make_float2(x[i], x[i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) store_from_f32(base, off + i, dtype, x[i]);
-  }
-}
-
 // Lookup tables of the tiles: entry e at row e, K in the first half of a row, V in the second,
 // one copy a lane.  BITS <= 4: half2 of a code pair; 8 bits: half2(hi, lo) of a code.  A warp
 // makes 32 entries at a time, one a lane, and writes each to its row.
 template <int BITS, int HALF>
-__device__ __forceinline__ void tiles_lut(uint8_t* lut, const float* c, float alpha, int warp, int lane) {
+__device__ __forceinline__ void tiles_lut(uint8_t* lut, const float* c, float alpha, int warp, int warps,
+                                          int lane) {
   constexpr int kEntries = lut_entries(BITS);
-  for (int e0 = warp * 32; e0 < kEntries; e0 += kTilesThreads) {
+  for (int e0 = warp * 32; e0 < kEntries; e0 += warps * 32) {
     const int e = e0 + lane;
     uint32_t v = 0u;
     if (e < kEntries) {
@@ -272,21 +217,111 @@ __device__ __forceinline__ void tiles_lut(uint8_t* lut, const float* c, float al
 }
 // The factor whose scaled centroids lie nearest to fp16 numbers: 1 + best / 512.
 template <int BITS>
-__device__ __forceinline__ void tiles_alpha(const float* c, int tid, unsigned long long* best) {
+__device__ __forceinline__ void tiles_alpha(const float* c, int t, int threads, unsigned long long* best) {
   if constexpr (BITS <= 4) {
-    const float a = 1.0f + (float)tid * (1.0f / kTilesThreads);
-    float err = 0.f;
-    for (int i = 0; i < 1 << BITS; ++i) {
-      const float x = c[i] * a, d = __half2float(__float2half_rn(x)) - x;
-      err = fmaf(d, d, err);
+    unsigned long long key = ~0ull;
+    for (int j = t; j < 512; j += threads) {
+      const float a = 1.0f + (float)j * (1.0f / 512);
+      float err = 0.f;
+      for (int i = 0; i < 1 << BITS; ++i) {
+        const float x = c[i] * a, d = __half2float(__float2half_rn(x)) - x;
+        err = fmaf(d, d, err);
+      }
+      const unsigned long long k = ((unsigned long long)__float_as_uint(err / (a * a)) << 32) | (unsigned)j;
+      key = k < key ? k : key;
     }
-    unsigned long long key = ((unsigned long long)__float_as_uint(err / (a * a)) << 32) | (unsigned)tid;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
       key = other < key ? other : key;
     }
-    if ((tid & 31) == 0) atomicMin(best, key);
+    if ((t & 31) == 0) atomicMin(best, key);
+  }
+}
+__device__ __forceinline__ float tiles_factor(unsigned long long best) {
+  return 1.0f + (float)(unsigned)best * (1.0f / 512);
+}
+
+// A row of D coordinates over D / 16 lanes: lane l of the group holds, in x[4 j + e], coordinate
+// 4 (l + D / 16 j) + e, so that a group's accesses of 4 coordinates a lane are contiguous.
+template <int D>
+__device__ __forceinline__ int group_coord(int l, int j) { return 4 * (l + D / 16 * j); }
+// FWHT of such a row (natural order, no scaling).
+template <int D>
+__device__ __forceinline__ void group_fwht(float (&x)[16], int l) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i & h) == 0) {
+        const float a = x[i], b = x[i + h];
+        x[i] = a + b;
+        x[i + h] = a - b;
+      }
+#pragma unroll
+  for (int m = 1; m < D / 16; m <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
+      x[i] = (l & m) ? o - x[i] : x[i] + o;
+    }
+}
+// The signs of the coordinates that a lane holds, a bit each.
+template <int D>
+__device__ __forceinline__ uint32_t group_signs(uint64_t seed, int l) {
+  uint32_t s = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    s |= (sign_mask_at(seed, group_coord<D>(l, i / 4) + i % 4) >> 31) << i;
+  return s;
+}
+__device__ __forceinline__ void group_flip(float (&x)[16], uint32_t signs) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((signs << (31 - i)) & 0x80000000u));
+}
+// Its elements from / to memory; vec: rows start on 16-byte boundaries.
+template <int D>
+__device__ __forceinline__ void group_load(float (&x)[16], const void* base, int64_t off, int32_t dtype,
+                                           bool vec, int l) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t at = off + group_coord<D>(l, j);
+    if (vec && dtype != TQ_F32) {
+      const uint2 w = *(const uint2*)((const uint16_t*)base + at);
+      if (dtype == TQ_BF16) {
+        x[4 * j] = __uint_as_float(w.x << 16), x[4 * j + 1] = __uint_as_float(w.x & 0xffff0000u);
+        x[4 * j + 2] = __uint_as_float(w.y << 16), x[4 * j + 3] = __uint_as_float(w.y & 0xffff0000u);
+      } else {
+        const float2 a = __half22float2(*(const __half2*)&w.x), b = __half22float2(*(const __half2*)&w.y);
+        x[4 * j] = a.x, x[4 * j + 1] = a.y, x[4 * j + 2] = b.x, x[4 * j + 3] = b.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * j + e] = load_as_f32(base, at + e, dtype);
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ void group_store(const float (&x)[16], void* base, int64_t off, int32_t dtype,
+                                            bool vec, int l) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t at = off + group_coord<D>(l, j);
+    if (vec && dtype != TQ_F32) {
+      uint2 w;
+      if (dtype == TQ_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[4 * j], x[4 * j + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[4 * j + 2], x[4 * j + 3]);
+        w = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
+      } else {
+        w = make_uint2(pack_half2(x[4 * j], x[4 * j + 1]), pack_half2(x[4 * j + 2], x[4 * j + 3]));
+      }
+      *(uint2*)((uint16_t*)base + at) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) store_from_f32(base, at + e, dtype, x[4 * j + e]);
+    }
   }
 }
 
@@ -310,11 +345,11 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-template <int D, int KB, int VB, bool PREC>
+template <int D, int KB, int VB>
 __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const AttendParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  using C = TilesCfg<D, KB, VB, PREC>;
+  using C = TilesCfg<D, KB, VB>;
   constexpr int N = C::N, NI = C::NI, PART = C::PART, E = D / 32;
   constexpr int KPACK = D * KB / 8, VPACK = D * VB / 8;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -324,7 +359,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   float* norm_s = (float*)(lut + C::LUT);                // [2][K, V][N]
   TilesMisc* ms = (TilesMisc*)(lut + C::LUT + C::NORMS);
   float* part_s = (float*)smem;                          // [slot][row][PART], at the end
-  float* qs_s = (float*)(ring_s + (C::RING - 1) * C::STAGE);   // until the first tiles come
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = (int)cluster.num_blocks(), split = (int)cluster.block_rank();
   const int b = blockIdx.x / ctas, kvh = blockIdx.y, G = p.group;
@@ -368,105 +402,91 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       mbar_init(&ms->ring_empty[i], two ? 2 : 1);
     }
     mbar_init(&ms->o_done, kIssuers);
-    ms->best[0] = ms->best[1] = ~0ull;
+    mbar_init(&ms->q_ready, 8);                          // the softmax warps
+    ms->best = ~0ull;
     fence_mbar_init();
   }
   if (warp == 12) tmem_alloc(&ms->tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (PREC) {
-    tiles_alpha<KB>(p.kc, tid, &ms->best[0]);
-    tiles_alpha<VB>(p.vc, tid, &ms->best[1]);
-  }
-  // q' of a row by a warp: sign flips, FWHT, 1/sqrt(D), to unit length, fp16 (hi, lo)
-  {
-    uint32_t sgn[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      sgn[i] = sign_mask_at(p.sign_seed, lane * E + i) ^ (p.scale_log2 < 0.f ? 0x80000000u : 0u);
-    constexpr int B = 4;
-    const int all = two ? 2 * kTileRows : kTileRows;
-    for (int rb = warp * B; rb < all; rb += kTilesWarps * B) {
-      float x[B][E];
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const int r = rb + j, rr = r0 + r;
-        const int64_t off = (int64_t)(sq.row0 + rr / G) * p.q_rstride +
-                            (int64_t)(kvh * G + rr % G) * p.q_hstride + lane * E;
-        if (r < rows) {
-          load_run<E>(x[j], p.q, off, p.q_dtype, p.q_vec);
-        } else {
-#pragma unroll
-          for (int i = 0; i < E; ++i) x[j][i] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const int r = rb + j;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[j][i] = __uint_as_float(__float_as_uint(x[j][i]) ^ sgn[i]);
-        warp_fwht<E>(x[j], lane);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          x[j][i] *= inv_sqrt_dim<D>();
-          ss = fmaf(x[j][i], x[j][i], ss);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float nrm = sqrtf(ss), inv = nrm > 0.f ? 1.0f / nrm : 0.f;
-        uint8_t* qt = q_s + (r / kTileRows) * C::QPARTS * C::QTILE;
-        const int row = r % kTileRows;
-        uint32_t hi[E / 2], lo[E / 2];
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const float u = x[j][2 * i] * inv, v = x[j][2 * i + 1] * inv;
-          hi[i] = pack_half2(u, v);
-          const float2 h = __half22float2(*(const __half2*)&hi[i]);
-          lo[i] = pack_half2(u - h.x, v - h.y);
-        }
-        // E consecutive columns: inside one 16-byte chunk
-        uint32_t* dst = (uint32_t*)(qt + sw128_offset(row, lane * E, kTileRows));
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) dst[i] = hi[i];
-        if constexpr (PREC) {
-          dst = (uint32_t*)(qt + C::QTILE + sw128_offset(row, lane * E, kTileRows));
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) dst[i] = lo[i];
-        }
-        if (lane == 0) qs_s[r] = nrm * fabsf(p.scale_log2);
-      }
-    }
-  }
-  __syncthreads();                                       // the best factors are known
-  const float ak = PREC && KB <= 4 ? 1.0f + (float)(unsigned)ms->best[0] * (1.0f / kTilesThreads) : 1.0f;
-  const float av = PREC && VB <= 4 ? 1.0f + (float)(unsigned)ms->best[1] * (1.0f / kTilesThreads) : 1.0f;
-  tiles_lut<KB, 0>(lut, p.kc, ak, warp, lane);
-  tiles_lut<VB, 1>(lut, p.vc, av, kTilesWarps - 1 - warp, lane);
-  const int srow = tid & (kTileRows - 1);                // a softmax thread's row in its slot
-  float qs = 0.f;
-  int myrow = srow;
-  if (warp < 8) {
-    myrow = two ? (warp >> 2) * kTileRows + srow : srow;
-    qs = qs_s[myrow] / ak;
-  }
-  fence_proxy_async_smem();                              // q is read by the tensor cores
-  __syncthreads();
   const uint32_t tmem = ms->tmem;
+  const int srow = tid & (kTileRows - 1);                // a softmax thread's row in its slot
+  const int myrow = two && warp < 8 ? (warp >> 2) * kTileRows + srow : srow;
+  float qs = 0.f;                                        // |q'| |scale| log2(e) of the row
+  float ak = 1.0f;                                       // the factor of the key centroids
+  float* qs_s = C::kOneO ? (float*)(ring_s + (C::RING - 1) * C::STAGE) : norm_s + 2 * N;
+  // q' of the rows, a group of lanes each: sign flips, FWHT, 1/sqrt(D), to unit length in fp16
+  // into the operand; its scale to qs_s
+  auto make_q = [&](int w, int warps) {
+    const int l = lane % C::LPR;
+    const uint32_t signs = group_signs<D>(p.sign_seed, l);
+    const int all = two ? 2 * kTileRows : kTileRows;
+    auto load = [&](float (&x)[16], int r) {
+      const int t = (r0 + r) / G, g = r0 + r - t * G;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = 0.f;
+      if (r < rows)
+        group_load<D>(x, p.q, (int64_t)(sq.row0 + t) * p.q_rstride + (int64_t)(kvh * G + g) * p.q_hstride,
+                      p.q_dtype, p.q_vec, l);
+    };
+    float next[16];
+    load(next, w * C::RPI + lane / C::LPR);
+#pragma unroll 1
+    for (int rb = w * C::RPI; rb < all; rb += warps * C::RPI) {
+      const int r = rb + lane / C::LPR;
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = next[i];
+      load(next, rb + warps * C::RPI < all ? r + warps * C::RPI : rows);
+      group_flip(x, signs);
+      group_fwht<D>(x, l);
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int m = 1; m < C::LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      const float nrm = sqrtf(ss), inv = nrm > 0.f ? copysignf(1.0f / nrm, p.scale_log2) : 0.f;
+      uint8_t* qt = q_s + (r / kTileRows) * C::QTILE;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = sw128_offset(r % kTileRows, group_coord<D>(l, j), kTileRows);
+        const float a = x[4 * j] * inv, b = x[4 * j + 1] * inv, c = x[4 * j + 2] * inv, d = x[4 * j + 3] * inv;
+        *(uint2*)(qt + at) = make_uint2(pack_half2(a, b), pack_half2(c, d));
+      }
+      if (l == 0) qs_s[r] = nrm * inv_sqrt_dim<D>() * fabsf(p.scale_log2);
+    }
+  };
+  if constexpr (C::kOneO) {
+    // D = 256: a thread cannot hold a row; every warp takes rows, then the tables
+    tiles_alpha<KB>(p.kc, tid, kTilesThreads, &ms->best);
+    make_q(warp, kTilesWarps);
+    __syncthreads();                                     // the best factors are known
+    if (KB <= 4) ak = tiles_factor(ms->best);
+    tiles_lut<KB, 0>(lut, p.kc, ak, warp, kTilesWarps, lane);
+    tiles_lut<VB, 1>(lut, p.vc, 1.0f, kTilesWarps - 1 - warp, kTilesWarps, lane);
+    if (warp < 8) qs = qs_s[srow] / ak;
+    fence_proxy_async_smem();                            // q is read by the tensor cores
+    __syncthreads();
+  }
   // tensor memory: O' of slot j at columns j D, its scores (and weights) at 256 + 128 j, 64 a buffer
   auto fail = [&]() {
     report_error(p.err, TQ_DEVERR_TIMEOUT);
   };
   // norm buffers
-  float* norms = C::NBUF == 2 && !PREC && !two ? (float*)(q_s + C::QTILE) : norm_s;
-  const int nmask = PREC || two ? 1 : 3, nshift = PREC || two ? 1 : 2;
+  float* norms = !C::kOneO && !two ? (float*)(q_s + C::QTILE) : norm_s;
+  const int nmask = two ? 1 : 3, nshift = two ? 1 : 2;
   // ring position of a tile's K and V
   auto k_at = [&](int k) { return two ? 2 * k : (k == 0 ? 0 : 2 * k - 1); };
   auto v_at = [&](int k) { return two ? 2 * k + 1 : 2 * k + 2; };
 
   if (warp >= 12) {
     regs_dec<kIssueRegs>();
+    if constexpr (!C::kOneO) {
+      make_q(warp - 4, 12);
+      fence_proxy_async_smem();                          // q is read by the tensor cores
+      asm volatile("bar.sync 2, 384;" ::: "memory");
+    }
     // The whole warp walks the loop, so that descriptors stay in uniform registers; one thread
     // issues.
     const int uwarp = __shfl_sync(0xffffffffu, warp, 0);
@@ -474,10 +494,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       const bool leader = elect_one();
       const int slot = uwarp - 12, items = slot_tiles(slot) * C::H;
       const uint32_t acc = tmem + slot * D, s_at = tmem + 256 + slot * 128;
-      const uint64_t q = sw128_desc(smem_u32(q_s) + (two ? slot * C::QPARTS * C::QTILE : 0));
+      const uint64_t q = sw128_desc(smem_u32(q_s) + (two ? slot * C::QTILE : 0));
       const uint32_t ring_at = smem_u32(ring_s);
-      bool ok = true;
-      for (int n = 0; n < items + 2; ++n) {
+      bool ok = C::kOneO || tile_wait(&ms->q_ready, 0, p.wait_ms);
+      for (int n = 0; n < items + 2 && __all_sync(0xffffffffu, ok); ++n) {
         if (n >= 2) {                                    // P V of item n - 2
           const int m = n - 2, at = v_at(slot_tile(slot, m / C::H)), sl = at % C::RING, half = m % C::H;
           ok = (half || tile_wait(&ms->ring_full[sl], (uint32_t)(at / C::RING) & 1u, p.wait_ms)) &&
@@ -507,8 +527,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
               const uint64_t ko = kd + (ks >> 2) * (N * 8) + (ks & 3) * 2;
               const uint32_t to = s_at + (n & 1) * 64;
               umma_bf16(to, qd, ko, f16_idesc(NI, false), ks > 0 ? 1u : 0u);
-              if constexpr (PREC) umma_bf16(to, qd + C::QTILE / 16, ko, f16_idesc(NI, false), 1u);
-              if constexpr (C::kKeyLo) umma_bf16(to, qd, ko + (D / 64) * (N * 8), f16_idesc(NI, false), 1u);
             }
             umma_commit(&ms->s_full[slot][n & 1]);
             if (half == C::H - 1) umma_commit(&ms->ring_empty[sl]);
@@ -580,8 +598,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     auto look = [&](uint32_t a) { return *(const uint32_t*)(lut + a); };
     const uint32_t lk = 4u * lane, lv = 128u + 4u * lane;
     // 16 codes to 16 halves
-    auto look_up = [&](auto IV, auto IL, const auto& raw, int i, uint32_t (&h)[8]) {
-      constexpr bool V = decltype(IV)::value, LO = decltype(IL)::value;
+    auto look_up = [&](auto IV, const auto& raw, int i, uint32_t (&h)[8]) {
+      constexpr bool V = decltype(IV)::value;
       constexpr int BITS = V ? VB : KB, W = V ? C::VW : C::KW;
       const uint32_t off = V ? lv : lk;
       uint32_t r[W];
@@ -593,31 +611,26 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
           h[j] = look(lut_addr<2 * j * BITS, 2 * BITS>(r, off));
         } else {
           h[j] = __byte_perm(look(lut_addr<2 * j * BITS, BITS>(r, off)),
-                             look(lut_addr<(2 * j + 1) * BITS, BITS>(r, off)), LO ? 0x7632 : 0x5410);
+                             look(lut_addr<(2 * j + 1) * BITS, BITS>(r, off)), 0x5410);
         }
       });
     };
     // ... stored as two 16-byte chunks of the row; the order in which a lane stores its two
     // keeps 8 lanes on 8 chunks
-    auto store_row = [&](auto IL, const uint32_t (&h)[8], int i, uint8_t* stage) {
-      constexpr bool LO = decltype(IL)::value;
+    auto store_row = [&](const uint32_t (&h)[8], int i, uint8_t* stage) {
       const int row = rbase + i * C::RPI;
-      uint8_t* dst = stage + (l >> 2) * (N * 128) + row * 128 + (LO ? (D / 64) * (N * 128) : 0);
+      uint8_t* dst = stage + (l >> 2) * (N * 128) + row * 128;
       const int c0 = 2 * (l & 3), odd = D > 64 ? (l >> 2) & 1 : 0;
       const uint4 v0 = make_uint4(h[0], h[1], h[2], h[3]), v1 = make_uint4(h[4], h[5], h[6], h[7]);
       *(uint4*)(dst + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? v1 : v0;
       *(uint4*)(dst + (((c0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? v0 : v1;
     };
-    // ... times the norm of the row (mul: this lane's row's, two halves hi + lo for K)
-    auto scale_row = [&](auto IV, uint32_t (&h)[8], uint32_t mul, int i) {
-      constexpr bool V = decltype(IV)::value;
+    // ... times the norm of the row (mul: this lane's row's, twice)
+    auto scale_row = [&](uint32_t (&h)[8], uint32_t mul, int i) {
       const uint32_t m = __shfl_sync(0xffffffffu, mul, i * C::RPI + rsub);
-      const uint32_t a = __byte_perm(m, 0, 0x1010), b = __byte_perm(m, 0, 0x3232);
-      const __half2 hi = *(const __half2*)&a, lo = *(const __half2*)&b;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const __half2 c = *(const __half2*)&h[j];
-        const __half2 x = V ? __hmul2(c, hi) : __hfma2(c, hi, __hmul2(c, lo));
+        const __half2 x = __hmul2(*(const __half2*)&h[j], *(const __half2*)&m);
         h[j] = *(const uint32_t*)&x;
       }
     };
@@ -638,13 +651,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         nv = *(const float*)(sl + p.k_region + VPACK);
       }
     };
-    // Norms and facts of tile k for the softmax warps; kmul, vmul: the factors of this lane's
-    // row in the operands (halves hi and lo; 1 and 0 where the softmax applies the norms).
-    uint32_t kmul = 0x00003c00u, vmul = 0x00003c00u;
+    // Norms and facts of tile k for the softmax warps; vmul: the factor of this lane's row in the
+    // V operand, twice (1 where the softmax applies the norms).
+    uint32_t vmul = 0x3c003c00u;
     auto publish = [&](int k) {
+      // the second buffer holds the scales of q until they are read
+      if (!C::kOneO && k == 1) tile_wait(&ms->q_ready, 0, p.wait_ms);
       const int buf = k & nmask, mb = k & 1;
       bool ok = true;
-      int kmax = -100, kmin = 1000, vmax = -100, vmin = 1000;
+      int vmax = -100, vmin = 1000;
       if (lane < N / kDequantWarps) {
         norms[buf * 2 * N + nrow] = nk;
         norms[buf * 2 * N + N + nrow] = nv;
@@ -652,41 +667,25 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         const int tok = first + nrow % kBlockSize;
         ok = first >= 0 && tok <= pos_first && (tok >= low_last || tok < p.sinks) && isfinite(nk) &&
              isfinite(nv);
-        kmax = (int)ceilf(fmaxf(log2_bound(fabsf(nk)), -100.0f));
         vmax = (int)ceilf(fmaxf(log2_bound(fabsf(nv)), -100.0f));
-        if (nk != 0.f) kmin = kmax;
         if (nv != 0.f) vmin = vmax;
       }
-      kmax = __reduce_max_sync(0xffffffffu, kmax);
-      kmin = __reduce_min_sync(0xffffffffu, kmin);
       vmax = __reduce_max_sync(0xffffffffu, vmax);
       vmin = __reduce_min_sync(0xffffffffu, vmin);
       ok = __all_sync(0xffffffffu, ok);
-      if (lane == 0) ms->meta[mb][w] = TileMeta{kmax, kmin, vmax, vmin, ok ? 1 : 0};
+      if (lane == 0) ms->meta[mb][w] = TileMeta{vmax, vmin, ok ? 1 : 0};
       asm volatile("bar.sync 1, 128;" ::: "memory");     // the dequantizing warps
 #pragma unroll
       for (int i = 0; i < kDequantWarps; ++i) {
         const TileMeta m = ms->meta[mb][i];
         ok = ok && m.plain;
-        kmax = max(kmax, m.kmax);
-        kmin = min(kmin, m.kmin);
         vmax = max(vmax, m.vmax);
         vmin = min(vmin, m.vmin);
       }
       ok = ok && vmax - vmin <= 8 && abs(vmax) < 60;
-      float ks = 1.0f;
-      if constexpr (!PREC) {
-        ok = ok && kmax - kmin <= 8 && abs(kmax) < 60;
-        kmul = vmul = 0x00003c00u;
-        if (ok) {
-          const float sk = nk * __int_as_float((127 - kmax) << 23);
-          const float hi = __half2float(__float2half_rn(sk));
-          kmul = pack_half2(hi, sk - hi);
-          vmul = pack_half2(nv * __int_as_float((127 - vmax) << 23), 0.f);
-          ks = __int_as_float((127 + kmax) << 23);
-        }
-      }
-      if (w == 0 && lane == 0) ms->info[buf] = TileInfo{ok ? 1 : 0, ks, (float)vmax};
+      const float v = ok ? nv * __int_as_float((127 - vmax) << 23) : 1.0f;
+      vmul = pack_half2(v, v);
+      if (w == 0 && lane == 0) ms->info[buf] = TileInfo{ok ? 1 : 0, (float)vmax};
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->norm_full[buf]);
     };
@@ -711,19 +710,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       for (int i = 0; i < C::IT; i += U) {
         uint32_t h[U][8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) look_up(IV, std::false_type{}, raw, i + u, h[u]);
-        if constexpr (!PREC) {
+        for (int u = 0; u < U; ++u) look_up(IV, raw, i + u, h[u]);
+        if constexpr (V) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) scale_row(IV, h[u], mul, i + u);
+          for (int u = 0; u < U; ++u) scale_row(h[u], mul, i + u);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) store_row(std::false_type{}, h[u], i + u, stage);
-        if constexpr (C::kKeyLo && !V) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) look_up(IV, std::true_type{}, raw, i + u, h[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u) store_row(std::true_type{}, h[u], i + u, stage);
-        }
+        for (int u = 0; u < U; ++u) store_row(h[u], i + u, stage);
         if (more) {
 #pragma unroll
           for (int u = 0; u < U; ++u) load_rows(INV, coming, i + u, next, at);
@@ -747,6 +740,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       load_norms(0, b0);
       load_all(KI{}, raw_k, b0);
       if constexpr (C::kDeep) load_all(VI{}, raw_v, b0);
+      if constexpr (!C::kOneO) {                         // the tables, while these come in
+        tiles_lut<VB, 1>(lut, p.vc, 1.0f, w, kDequantWarps, lane);
+        tiles_alpha<KB>(p.kc, tid - 256, 128, &ms->best);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (KB <= 4) ak = tiles_factor(ms->best);
+        if (tid == 256) ms->alpha = ak;                  // read past norm_full
+        tiles_lut<KB, 0>(lut, p.kc, ak, w, kDequantWarps, lane);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
       if (two) {                                         // K(0), V(0), K(1), V(1), ...
         for (int k = 0; k < tiles; ++k) {
           const bool more = k + 1 < tiles;
@@ -759,8 +761,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
             b1 = fetch(k + 1);
             load_norms(k + 1, b1);
           }
-          if constexpr (C::kDeep) produce(KI{}, raw_k, KI{}, raw_k, k_at(k), kmul, more, b1);
-          else produce(KI{}, raw_k, VI{}, raw_v, k_at(k), kmul, true, b0);
+          if constexpr (C::kDeep) produce(KI{}, raw_k, KI{}, raw_k, k_at(k), 0u, more, b1);
+          else produce(KI{}, raw_k, VI{}, raw_v, k_at(k), 0u, true, b0);
           ok = free_stage(v_at(k));
           if (!ok) break;
           if constexpr (C::kDeep) produce(VI{}, raw_v, VI{}, raw_v, v_at(k), vmul, more, b1);
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
           b1 = fetch(1);
           load_norms(1, b1);
         }
-        produce(KI{}, raw_k, KI{}, raw_k, k_at(0), kmul, tiles > 1, b1);
+        produce(KI{}, raw_k, KI{}, raw_k, k_at(0), 0u, tiles > 1, b1);
         if (!C::kDeep && tiles == 1) load_all(VI{}, raw_v, b0);
         for (int k = 0; k < tiles; ++k) {
           vmul_now = vmul;
@@ -783,24 +785,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
           if (more1) {
             ok = free_stage(k_at(k + 1));
             if (!ok) break;
-            if constexpr (!PREC) {
-              // the norms' buffer: item k - 3 is past its P V (its V's stage was K(k)'s)
-              publish(k + 1);
-              if (more2) load_norms(k + 2, b2);
-            }
-            if constexpr (C::kDeep) produce(KI{}, raw_k, KI{}, raw_k, k_at(k + 1), kmul, more2, b2);
-            else produce(KI{}, raw_k, VI{}, raw_v, k_at(k + 1), kmul, true, b0);
-            if constexpr (PREC) {
-              // the norms' buffer is free once the last item of tile k - 1 has its weights
-              if (k >= 1) {
-                const int j = C::kOneO ? 0 : (k - 1) & 1;
-                const int m = (C::kOneO ? k - 1 : (k - 1) >> 1) * C::H + C::H - 1;
-                ok = tile_wait(&ms->p_ready[j][m & 1], (uint32_t)(m >> 1) & 1u, p.wait_ms);
-              }
-              if (!ok) break;
-              publish(k + 1);
-              if (more2) load_norms(k + 2, b2);
-            }
+            // the norms' buffer: tile k - 3 is past its P V (its V's stage was K(k)'s)
+            publish(k + 1);
+            if (more2) load_norms(k + 2, b2);
+            if constexpr (C::kDeep) produce(KI{}, raw_k, KI{}, raw_k, k_at(k + 1), 0u, more2, b2);
+            else produce(KI{}, raw_k, VI{}, raw_v, k_at(k + 1), 0u, true, b0);
           }
           ok = free_stage(v_at(k));
           if (!ok) break;
@@ -820,6 +809,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     // ---- softmax: a thread = a row of slot warp / 4 ----
     regs_inc<kSoftmaxRegs>();
     const int slot = warp >> 2;
+    if constexpr (!C::kOneO) {
+      make_q(warp, 12);
+      asm volatile("bar.sync 2, 384;" ::: "memory");     // the warps that made q
+      qs = qs_s[myrow];
+      fence_proxy_async_smem();                          // q is read by the tensor cores
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->q_ready);
+    }
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's quarter of tensor memory
     float M = -INFINITY, sum = 0.f;
     const int pos = myrow < rows ? p0 + (r0 + myrow) / G : -1;
@@ -836,13 +833,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         ok = false;
         break;
       }
+      if (!C::kOneO && n == 0) qs /= ms->alpha;
       tc_fence_after();
       float s[NI];
       const float* nks = norms + nb * 2 * N + half * NI;
       const float* nvs = nks + N;
       const TileInfo info = ms->info[nb];
       const bool plain = info.plain;
-      const float qt = qs * info.ek_scale;
       // x of 16 columns at c, key by key: norms and masks here (a tile that is not plain)
       auto masked = [&](int c, float (&x)[16]) {
         tmem_ld16_nowait(s_at + c, x);
@@ -871,20 +868,18 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
           }
 #pragma unroll
           for (int c = h; c < h + HL; c += 8) {
-            if constexpr (PREC) {
 #pragma unroll
-              for (int i = c; i < c + 8; i += 4) {
-                const float4 f = *(const float4*)(nks + i);
-                const float2 u = mul2(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
-                const float2 v = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
-                s[i] = u.x, s[i + 1] = u.y, s[i + 2] = v.x, s[i + 3] = v.y;
-              }
+            for (int i = c; i < c + 8; i += 4) {
+              const float4 f = *(const float4*)(nks + i);
+              const float2 u = mul2(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
+              const float2 v = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
+              s[i] = u.x, s[i + 1] = u.y, s[i + 2] = v.x, s[i + 3] = v.y;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) zz[j] = max3(zz[j], s[c + 2 * j], s[c + 2 * j + 1]);
           }
         }
-        z = fmaf(max3(fmaxf(zz[0], zz[1]), zz[2], zz[3]), qt, info.ev);
+        z = fmaf(max3(fmaxf(zz[0], zz[1]), zz[2], zz[3]), qs, info.ev);
       } else {
 #pragma unroll 1
         for (int c = 0; c < NI; c += 16) {
@@ -920,9 +915,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       const float ref = M == -INFINITY ? 0.f : M;
       uint32_t pk[8];
       if (plain) {
-        // without PREC: P = 2^(x + ev - M), the norms (over 2^ev) are in the operands
-        const float shift = PREC ? -ref : info.ev - ref;
-        const float2 q2 = make_float2(qt, qt), m2 = make_float2(shift, shift);
+        // P = 2^(x + ev - M): the norms over 2^ev are in the operand
+        const float shift = info.ev - ref;
+        const float2 q2 = make_float2(qs, qs), m2 = make_float2(shift, shift);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0, l2 = l0, l3 = l0;
 #pragma unroll
         for (int c = 0; c < NI; c += 8) {
@@ -935,21 +930,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
           l1 = add2(l1, u[1]);
           l2 = add2(l2, u[2]);
           l3 = add2(l3, u[3]);
-          if constexpr (PREC) {
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const float4 f = *(const float4*)(nvs + c + 2 * j);
-              u[j] = mul2(u[j], make_float2(f.x, f.y));
-              u[j + 1] = mul2(u[j + 1], make_float2(f.z, f.w));
-            }
-          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) pk[c / 2 % 8 + j] = pack_half2(u[j].x, u[j].y);
           if (c % 16 == 8) tmem_st8(s_at + c / 16 * 8, pk);
         }
         l0 = add2(add2(l0, l1), add2(l2, l3));
         const float part = l0.x + l0.y;
-        sum = PREC ? sum + part : fmaf(part, __int_as_float((127 - (int)info.ev) << 23), sum);
+        sum = fmaf(part, __int_as_float((127 - (int)info.ev) << 23), sum);
       } else {
 #pragma unroll 1
         for (int c = 0; c < NI; c += 16) {                // P of a chunk lies over scores already read
@@ -978,17 +965,18 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     if (!(C::kOneO && slot)) {
       float* rec = part_s + (slot * kTileRows + srow) * PART;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        float o[16];
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
         if (items > 0 && ok) {
           tmem_ld16_nowait(o_at + c, o);
+          tmem_ld16_nowait(o_at + c + 16, o + 16);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) *(float4*)(rec + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        for (int i = 0; i < 32; i += 4) *(float4*)(rec + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
       // a sum that is not a number must survive the join, which drops empty partials
       rec[D] = sum != sum && M == -INFINITY ? -3e38f : M;
@@ -1000,50 +988,45 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   tc_fence_after();
   if (warp == 12) tmem_dealloc(tmem, 512);
   if (ctas > 1) cluster.sync();
-  // row r is joined by CTA r % ctas of the cluster, by a warp; records: CTAs x slots
-  const int recs = two || C::kOneO ? 1 : 2;
-  constexpr int RB = 2;                   // rows of a warp at once
-  uint32_t sgn[E];
+  // row r is joined by CTA r % ctas of the cluster, by a group of lanes; records: CTAs x slots
+  const int recs = two || C::kOneO ? 1 : 2, l = lane % C::LPR;
+  const uint32_t signs = group_signs<D>(p.sign_seed, l);
+#pragma unroll 1
+  for (int rb = warp * C::RPI; rb * ctas < rows; rb += kTilesWarps * C::RPI) {
+    const int r = (rb + lane / C::LPR) * ctas + split, t = (r0 + r) / G, g = r0 + r - t * G;
+    float o[16], sum = 0.f, top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < E; ++i) sgn[i] = sign_mask_at(p.sign_seed, lane * E + i);
-  for (int rb = split + ctas * warp; rb < rows; rb += ctas * kTilesWarps * RB) {
-    float Mr[RB], lr[RB], o[RB][E];
-#pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      Mr[j] = -INFINITY;
-      lr[j] = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[j][i] = 0.f;
-      const int r = rb + j * ctas * kTilesWarps;
-      if (r >= rows) continue;
-      auto record = [&](int i, float& m, float& ll, float (&v)[E]) {
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    if (r < rows) {
+      auto record = [&](int i) -> const float* {
         const float* from = part_s + ((recs == 2 ? (i & 1) * kTileRows : 0) + r) * PART;
-        if (ctas > 1) from = cluster.map_shared_rank(from, recs == 2 ? i >> 1 : i);
-        m = from[D];
-        ll = from[D + 1];
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = from[lane * E + e];
+        return ctas > 1 ? cluster.map_shared_rank(from, recs == 2 ? i >> 1 : i) : from;
       };
-      if (ctas * recs == 1) record(0, Mr[j], lr[j], o[j]);
-      else fold_records<E>(ctas * recs, record, Mr[j], lr[j], o[j]);
+#pragma unroll 1
+      for (int i = 0; i < ctas * recs; ++i) top = fmaxf(top, record(i)[D]);
+#pragma unroll 1
+      for (int i = 0; i < ctas * recs; ++i) {
+        const float* from = record(i);
+        const float m = from[D], w = m == -INFINITY ? 0.f : exp2f(m - top);
+        sum = fmaf(w, from[D + 1], sum);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = *(const float4*)(from + group_coord<D>(l, j));
+          o[4 * j] = fmaf(w, v.x, o[4 * j]);
+          o[4 * j + 1] = fmaf(w, v.y, o[4 * j + 1]);
+          o[4 * j + 2] = fmaf(w, v.z, o[4 * j + 2]);
+          o[4 * j + 3] = fmaf(w, v.w, o[4 * j + 3]);
+        }
+      }
     }
+    const float inv = sum == 0.f ? 0.f : inv_sqrt_dim<D>() / sum;   // a row that sees nothing: 0
 #pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      const float inv = lr[j] == 0.f ? 0.f : 1.0f / (lr[j] * av);   // a row that sees nothing: 0
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[j][i] *= inv * inv_sqrt_dim<D>();
-      warp_fwht<E>(o[j], lane);
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[j][i] = __uint_as_float(__float_as_uint(o[j][i]) ^ sgn[i]);
-    }
-#pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      const int r = rb + j * ctas * kTilesWarps, rr = r0 + r;
-      if (r >= rows) continue;
-      const int64_t off = (int64_t)(sq.row0 + rr / G) * p.o_rstride +
-                          (int64_t)(kvh * G + rr % G) * p.o_hstride + lane * E;
-      store_run<E>(o[j], p.out, off, p.out_dtype, p.out_vec);
-    }
+    for (int i = 0; i < 16; ++i) o[i] *= inv;
+    group_fwht<D>(o, l);
+    group_flip(o, signs);
+    if (r < rows)
+      group_store<D>(o, p.out, (int64_t)(sq.row0 + t) * p.o_rstride + (int64_t)(kvh * G + g) * p.o_hstride,
+                     p.out_dtype, p.out_vec, l);
   }
   if (ctas > 1) cluster.sync();              // no CTA leaves while its partials may be read
 }
