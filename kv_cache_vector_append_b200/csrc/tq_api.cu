@@ -655,7 +655,7 @@ tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* 
   p.sinks = sinks;
   p.err = ds->err.load(std::memory_order_relaxed);
   p.wait_ms = kWaitMs;
-  return launch_attend_any((int)D, cb->k.bits, cb->v.bits, p, ds->info, as_stream(stream));
+  return launch_attend_any((int)D, cb->k.bits, cb->v.bits, p, as_stream(stream));
 }
 
 // What resize and fork have in common.

@@ -1,132 +1,153 @@
 // tq_attend_launch.cuh -- host-side launch of the attention over chunks and windows.
 #pragma once
 
+#include <algorithm>
+#include <atomic>
+
 #include "tq_attend_rows.cuh"
 #include "tq_attend_tiles.cuh"
 #include "tq_launch.cuh"
 
 namespace tq {
 
-template <int D, int KB, int VB>
-tq_status launch_rows_t(const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
-  auto kern = attend_rows_kernel<D, KB, VB>;
-  constexpr int smem = rows_smem(D, KB, VB);
+// Rows a KV head up to which the rows kernel is used (8 sequences of 4096 tokens, 32/8 heads of
+// 128, 4 bits: 16 rows 31 us against the tiles' 69 us, 64 rows 100 against 69).
+constexpr int kRowsMost = 32;
+
+// Launches the kernel as clusters of 1, 2, 4 or 8 CTAs that split the keys of a group of rows.  Of the
+// counts that leave a CTA `least` units of keys or more, the one is taken whose waves of CTAs
+// times a CTA's time are least; alone and joined are the times of a CTA's start and end in
+// units of keys, without and with a join.
+template <auto kern>
+tq_status launch_attend(const AttendParams& p, int64_t tiles, int threads, int smem, int64_t units,
+                        int alone, int joined, int least, cudaStream_t st) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  // CTAs a cluster: enough for two CTAs an SM, as long as each warp keeps two pages or more
-  const int tiles = (int)(((int64_t)p.max_q * p.group + kRowsMax - 1) / kRowsMax);
-  int64_t steps = p.max_blocks;
-  if (p.window > 0)
-    steps = std::min(steps, ((int64_t)p.window + p.max_q - 1) / kBlockSize + 2 +
-                                ((int64_t)p.sinks + kBlockSize - 1) / kBlockSize);
-  const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
-  int ctas = 1;
-  while (ctas < kRowsMaxCtas && groups * ctas < 2 * di.num_sms &&
-         (int64_t)ctas * kRowsWarps * 4 <= steps)
-    ctas *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.batch * ctas), (unsigned)p.h_kv, (unsigned)tiles);
-  cfg.blockDim = dim3(kRowsWarps * 32);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  auto grid = [&](int ctas) {
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    cfg.gridDim = dim3((unsigned)(p.batch * ctas), (unsigned)p.h_kv, (unsigned)tiles);
+  };
+  // clusters of each size that the GPU holds at once (a property of the kernel)
+  static std::atomic<int> fit[4];
+  const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
+  int best = 1;
+  int64_t best_cost = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int ctas = 1 << i;
+    if (i > 0 && units < (int64_t)ctas * least) break;
+    int n = fit[i].load(std::memory_order_relaxed);
+    if (n == 0) {
+      grid(ctas);
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return TQ_ERR_CUDA;
+      fit[i].store(n, std::memory_order_relaxed);
+    }
+    const int64_t cost = (groups + n - 1) / n * ((i ? joined : alone) + (units + ctas - 1) / ctas);
+    if (i == 0 || cost < best_cost) {
+      best = ctas;
+      best_cost = cost;
+    }
+  }
+  grid(best);
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return TQ_ERR_CUDA;
   return launch_status();
 }
 
+// Pages of the longest span of keys that `tokens` consecutive tokens may see.
+inline int64_t attend_pages(const AttendParams& p, int64_t tokens) {
+  if (p.window == 0) return p.max_blocks;
+  return std::min<int64_t>(p.max_blocks, (p.window + tokens) / kBlockSize + 2 +
+                                             ((int64_t)p.sinks + kBlockSize - 1) / kBlockSize);
+}
+
+template <int D, int KB, int VB, int NT>
+tq_status launch_rows_t(const AttendParams& p, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.max_q * p.group;
+  // start and end of a CTA: about 8 us, 48 pages of its eight warps
+  return launch_attend<attend_rows_kernel<D, KB, VB, NT>>(
+      p, (rows + 8 * NT - 1) / (8 * NT), kRowsWarps * 32, rows_smem(D, KB, VB, NT),
+      attend_pages(p, 8 * NT), 48, 48, kRowsWarps, st);
+}
+
 template <int D, int KB, int VB>
-tq_status launch_tiles_t(AttendParams p, const DeviceInfo& di, cudaStream_t st) {
+tq_status launch_tiles_t(AttendParams p, cudaStream_t st) {
   using C = TilesCfg<D, KB, VB>;
-  auto kern = attend_tiles_kernel<D, KB, VB>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return TQ_ERR_CUDA;
   // the split of registers between the warpgroups counts on the launch's own number
-  static const bool regs_ok = [&] {
+  static const bool regs_ok = [] {
     cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == kTilesRegs;
+    return cudaFuncGetAttributes(&a, attend_tiles_kernel<D, KB, VB>) == cudaSuccess && a.numRegs == kTilesRegs;
   }();
   if (!regs_ok) return TQ_ERR_CUDA;
   const int64_t rows = (int64_t)p.max_q * p.group;
   p.tile_rows = C::kTwoTiles && rows > kTileRows ? 2 * kTileRows : kTileRows;
-  const int tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
-  int64_t steps = p.max_blocks;
-  if (p.window > 0)
-    steps = std::min(steps, ((int64_t)p.window + p.tile_rows / p.group) / kBlockSize + 3 +
-                                ((int64_t)p.sinks + kBlockSize - 1) / kBlockSize);
-  // CTAs a cluster: until the grid fills the SMs twice, each keeping 512 keys or more
-  const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
-  int ctas = 1;
-  while (ctas < kTilesMaxCtas && groups * ctas < 2 * di.num_sms && (int64_t)ctas * 64 <= steps) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.batch * ctas), (unsigned)p.h_kv, (unsigned)tiles);
-  cfg.blockDim = dim3(kTilesThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return TQ_ERR_CUDA;
-  return launch_status();
+  const int64_t units = (attend_pages(p, p.tile_rows / p.group) + C::PPT - 1) / C::PPT;
+  // start and end of a CTA: about 16 us, or 35 us with a join, at 2.3 us a key tile
+  return launch_attend<attend_tiles_kernel<D, KB, VB>>(p, (rows + p.tile_rows - 1) / p.tile_rows,
+                                                       kTilesThreads, C::SMEM, units, 7, 15, 2, st);
 }
 
 // All V widths for one (head_dim, K width); instantiated in tq_attend_d<D>_k<KB>.cu so that
 // the kernels compile in parallel.
+template <int D, int KB, int VB>
+tq_status launch_rows_n(const AttendParams& p, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.max_q * p.group;
+  if constexpr (rows_tiles(D) == 4)
+    if (rows > 16) return launch_rows_t<D, KB, VB, 4>(p, st);
+  if constexpr (rows_tiles(D) >= 2)
+    if (rows > 8) return launch_rows_t<D, KB, VB, 2>(p, st);
+  return launch_rows_t<D, KB, VB, 1>(p, st);
+}
 template <int D, int KB>
-tq_status launch_rows_kbits(int vb, const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
+tq_status launch_rows_kbits(int vb, const AttendParams& p, cudaStream_t st) {
   switch (vb) {
-    case 2: return launch_rows_t<D, KB, 2>(p, di, st);
-    case 3: return launch_rows_t<D, KB, 3>(p, di, st);
-    case 4: return launch_rows_t<D, KB, 4>(p, di, st);
-    case 8: return launch_rows_t<D, KB, 8>(p, di, st);
+    case 2: return launch_rows_n<D, KB, 2>(p, st);
+    case 3: return launch_rows_n<D, KB, 3>(p, st);
+    case 4: return launch_rows_n<D, KB, 4>(p, st);
+    case 8: return launch_rows_n<D, KB, 8>(p, st);
     default: return TQ_ERR_UNSUPPORTED;
   }
 }
 
 template <int D, int KB>
-tq_status launch_tiles_kbits(int vb, const AttendParams& p, const DeviceInfo& di, cudaStream_t st) {
+tq_status launch_tiles_kbits(int vb, const AttendParams& p, cudaStream_t st) {
   switch (vb) {
-    case 2: return launch_tiles_t<D, KB, 2>(p, di, st);
-    case 3: return launch_tiles_t<D, KB, 3>(p, di, st);
-    case 4: return launch_tiles_t<D, KB, 4>(p, di, st);
-    case 8: return launch_tiles_t<D, KB, 8>(p, di, st);
+    case 2: return launch_tiles_t<D, KB, 2>(p, st);
+    case 3: return launch_tiles_t<D, KB, 3>(p, st);
+    case 4: return launch_tiles_t<D, KB, 4>(p, st);
+    case 8: return launch_tiles_t<D, KB, 8>(p, st);
     default: return TQ_ERR_UNSUPPORTED;
   }
 }
 
 #define TQ_DECLARE_TILES(D_, KB_)                                                          \
-  tq_status launch_tiles_d##D_##_k##KB_(int vb, const AttendParams& p, const DeviceInfo& di, \
-                                        cudaStream_t st);
+  tq_status launch_tiles_d##D_##_k##KB_(int vb, const AttendParams& p, cudaStream_t st);
 #define TQ_DEFINE_TILES(D_, KB_)                                                           \
-  tq_status launch_tiles_d##D_##_k##KB_(int vb, const AttendParams& p, const DeviceInfo& di, \
-                                        cudaStream_t st) {                                  \
-    return launch_tiles_kbits<D_, KB_>(vb, p, di, st);                                      \
+  tq_status launch_tiles_d##D_##_k##KB_(int vb, const AttendParams& p, cudaStream_t st) { \
+    return launch_tiles_kbits<D_, KB_>(vb, p, st);                                         \
   }
 TQ_FOR_EACH_DECODE(TQ_DECLARE_TILES)
 
 #define TQ_DECLARE_ROWS(D_, KB_)                                                          \
-  tq_status launch_rows_d##D_##_k##KB_(int vb, const AttendParams& p, const DeviceInfo& di, \
-                                       cudaStream_t st);
+  tq_status launch_rows_d##D_##_k##KB_(int vb, const AttendParams& p, cudaStream_t st);
 #define TQ_DEFINE_ROWS(D_, KB_)                                                           \
-  tq_status launch_rows_d##D_##_k##KB_(int vb, const AttendParams& p, const DeviceInfo& di, \
-                                       cudaStream_t st) {                                  \
-    return launch_rows_kbits<D_, KB_>(vb, p, di, st);                                      \
+  tq_status launch_rows_d##D_##_k##KB_(int vb, const AttendParams& p, cudaStream_t st) {  \
+    return launch_rows_kbits<D_, KB_>(vb, p, st);                                          \
   }
 TQ_FOR_EACH_DECODE(TQ_DECLARE_ROWS)
 
-inline tq_status launch_attend_any(int dim, int kb, int vb, const AttendParams& p,
-                                   const DeviceInfo& di, cudaStream_t st) {
-  const bool tiles = (int64_t)p.max_q * p.group > kRowsMax;
+inline tq_status launch_attend_any(int dim, int kb, int vb, const AttendParams& p, cudaStream_t st) {
+  const bool tiles = (int64_t)p.max_q * p.group > kRowsMost;
 #define TQ_ROWS_CASE(D_, KB_)                                                             \
   if (dim == D_ && kb == KB_)                                                             \
-    return tiles ? launch_tiles_d##D_##_k##KB_(vb, p, di, st) : launch_rows_d##D_##_k##KB_(vb, p, di, st);
+    return tiles ? launch_tiles_d##D_##_k##KB_(vb, p, st) : launch_rows_d##D_##_k##KB_(vb, p, st);
   TQ_FOR_EACH_DECODE(TQ_ROWS_CASE)
 #undef TQ_ROWS_CASE
   return TQ_ERR_UNSUPPORTED;
