@@ -2,7 +2,6 @@
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -392,20 +391,36 @@ def paged_decode_qjl(out, q, pages, block_table, seq_lens, codebooks: Codebooks,
            "tq_paged_decode_qjl")
 
 
-_NO_CONTEXT = contextlib.nullcontext()
-
-
-def _on_device(*tensors):
-    """A context in which the tensors' device (one for all) is the current one."""
-    torch = _torch()
-    _require_cuda(*tensors)
+def _descs(*tensors):
+    """Descriptors of CUDA tensors on one device, and its index."""
     index = tensors[0].get_device()
+    out = []
     for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("all tensors must live on a CUDA device (no CPU fallback)")
         if t.get_device() != index:
             raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device is needed")
+        out.append(_desc(t))
+    return out, index
+
+
+def _run(name: str, index: int, stream, args) -> None:
+    """An entry point on the tensors' device, on its current stream or the one given."""
+    torch = _torch()
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    entry = getattr(_load(), name)
     if index == torch.cuda.current_device():
-        return _NO_CONTEXT
-    return torch.cuda.device(index)
+        status = entry(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = entry(*args, handle)
+    if status != OK:
+        raise TQError(status, name)
+
+
+def _check_codebooks(codebooks: Codebooks, index: int) -> None:
+    if codebooks.k_centroids.get_device() != index:
+        raise ValueError(f"codebooks on {codebooks.k_centroids.device}, tensors on cuda:{index}")
 
 
 def paged_attend(out, q, q_starts, pages, block_table, seq_lens, codebooks: Codebooks,
@@ -414,13 +429,10 @@ def paged_attend(out, q, q_starts, pages, block_table, seq_lens, codebooks: Code
     """tq_paged_attend: causal attention of each sequence's last tokens (rows q_starts[b] ..
     q_starts[b + 1] of q, at most max_q) over its packed pages, which hold them already; with
     window > 0 over the last ``window`` tokens and the first ``sinks`` ones."""
-    with _on_device(out, q, q_starts, pages, block_table, seq_lens, codebooks.k_centroids):
-        st = _stream_handle(stream, q.device)
-        _check(_load().tq_paged_attend(_desc(out), _desc(q), _desc(q_starts), _desc(pages),
-                                       _desc(block_table), _desc(seq_lens),
-                                       ctypes.byref(codebooks.desc), ctypes.c_uint64(sign_seed),
-                                       ctypes.c_float(scale), max_q, window, sinks, st),
-               "tq_paged_attend")
+    d, index = _descs(out, q, q_starts, pages, block_table, seq_lens)
+    _check_codebooks(codebooks, index)
+    _run("tq_paged_attend", index, stream,
+         (*d, ctypes.byref(codebooks.desc), sign_seed, scale, max_q, window, sinks))
 
 
 def paged_decode_window(out, q, pages, block_table, seq_lens, codebooks: Codebooks,
@@ -428,21 +440,19 @@ def paged_decode_window(out, q, pages, block_table, seq_lens, codebooks: Codeboo
                         stream=None) -> None:
     """tq_paged_decode_window: one new token a sequence over the last ``window`` packed tokens
     (itself included) and the first ``sinks`` ones."""
-    with _on_device(out, q, pages, block_table, seq_lens, codebooks.k_centroids):
-        st = _stream_handle(stream, q.device)
-        _check(_load().tq_paged_decode_window(_desc(out), _desc(q), _desc(pages),
-                                              _desc(block_table), _desc(seq_lens),
-                                              ctypes.byref(codebooks.desc),
-                                              ctypes.c_uint64(sign_seed), ctypes.c_float(scale),
-                                              window, sinks, st),
-               "tq_paged_decode_window")
+    d, index = _descs(out, q, pages, block_table, seq_lens)
+    _check_codebooks(codebooks, index)
+    _run("tq_paged_decode_window", index, stream,
+         (*d, ctypes.byref(codebooks.desc), sign_seed, scale, window, sinks))
 
 
-def _layer_descs(layers):
+def _run_pages(name: str, layers, tensors, stream, *args) -> None:
     layers = [layers] if hasattr(layers, "data_ptr") else list(layers)
     if not layers:
         raise ValueError("no page tensors")
-    return layers, (TensorDesc * len(layers))(*[_desc(t) for t in layers])
+    n = len(layers)
+    d, index = _descs(*layers, *tensors)
+    _run(name, index, stream, ((TensorDesc * n)(*d[:n]), n, *d[n:], *args))
 
 
 def pages_resize(layers, block_table, seq_lens, new_lens, ref_counts, moves, window: int = 0,
@@ -451,37 +461,22 @@ def pages_resize(layers, block_table, seq_lens, new_lens, ref_counts, moves, win
     shared, partly filled last page is copied first), entries released for those that shrink,
     and with window > 0 the pages that a sliding window no longer reaches.  ``layers``: one
     page tensor, or one a model layer."""
-    layers, descs = _layer_descs(layers)
-    with _on_device(block_table, seq_lens, new_lens, ref_counts, moves, *layers):
-        st = _stream_handle(stream, block_table.device)
-        _check(_load().tq_pages_resize(descs, len(layers), _desc(block_table), _desc(seq_lens),
-                                       _desc(new_lens), _desc(ref_counts), _desc(moves), window,
-                                       sinks, st),
-               "tq_pages_resize")
+    _run_pages("tq_pages_resize", layers, (block_table, seq_lens, new_lens, ref_counts, moves), stream,
+               window, sinks)
 
 
 def pages_fork(layers, block_table, seq_lens, ref_counts, parents, children, moves,
                stream=None) -> None:
     """tq_pages_fork: the empty sequence children[i] becomes a copy of parents[i]: full pages
     shared, a partly filled last page copied in every layer."""
-    layers, descs = _layer_descs(layers)
-    with _on_device(block_table, seq_lens, ref_counts, parents, children, moves, *layers):
-        st = _stream_handle(stream, block_table.device)
-        _check(_load().tq_pages_fork(descs, len(layers), _desc(block_table), _desc(seq_lens),
-                                     _desc(ref_counts), _desc(parents), _desc(children),
-                                     _desc(moves), st),
-               "tq_pages_fork")
+    _run_pages("tq_pages_fork", layers,
+               (block_table, seq_lens, ref_counts, parents, children, moves), stream)
 
 
 def pages_compact(layers, src_table, src_lens, positions, counts, dst_table, stream=None) -> None:
     """tq_pages_compact: token i < counts[b] of sequence b in dst_table's pages <- its token
     positions[b, i] in src_table's pages, in every layer."""
-    layers, descs = _layer_descs(layers)
-    with _on_device(src_table, src_lens, positions, counts, dst_table, *layers):
-        st = _stream_handle(stream, src_table.device)
-        _check(_load().tq_pages_compact(descs, len(layers), _desc(src_table), _desc(src_lens),
-                                        _desc(positions), _desc(counts), _desc(dst_table), st),
-               "tq_pages_compact")
+    _run_pages("tq_pages_compact", layers, (src_table, src_lens, positions, counts, dst_table), stream)
 
 
 def rotate_unit(u, norm, x, sign_seed: int, stream=None) -> None:

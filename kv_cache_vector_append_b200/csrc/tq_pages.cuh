@@ -5,19 +5,19 @@
 // free when its count is 0.  Pages are given out lowest index first, to the requests in
 // their order, so the result does not depend on how the grid runs.
 //
-// resize and fork are two launches.  The first (one cluster) decides and allocates: it
-// turns the counts into a bitmap of free pages in shared memory (each CTA a contiguous
-// part of the pool), joins the CTAs' totals over distributed shared memory, and lets
-// thread r of the demanded ranks find its page (a search in the prefix sums of the
-// bitmap's words, then the n-th set bit) and its request (a search in the prefix sums of
-// the demands).  The second (one CTA per sequence and layer) does what is long: page
-// copies, shared or released table entries, count updates (integer atomics, so their
-// order does not matter).  What the second needs to know of the first is in `moves`, a
-// tensor of the caller: {from, to} of a page copy, {-1, -1} for none, {-2, -2} for a
-// refused request.  No other state is kept between the launches or the calls.
+// resize and fork plan and allocate in one cluster: it turns the counts into a bitmap of free
+// pages in shared memory (each CTA a contiguous part of the pool), joins the CTAs' totals over
+// distributed shared memory, and lets thread r of the demanded ranks find its page (a search
+// in the prefix sums of the bitmap's words, then the n-th set bit) and its request (a search
+// in the prefix sums of the demands).  What follows is long: page copies, shared or released
+// table entries, count updates (integer atomics, so their order does not matter).  Where it is
+// little (see kFusedChunks) the cluster's warps do it themselves after a cluster barrier, else
+// a second launch with a CTA per sequence and layer.  What that needs to know of the plan is
+// in `moves`, a tensor of the caller: {from, to} of a page copy, {-1, -1} for none, {-2, -2}
+// for a refused request.  No other state is kept between the launches or the calls.
 //
-// Bound: the first launch by latency (a few dependent reads and cluster barriers; the
-// pool is read once), the second and compact by memory bandwidth.
+// Bound: the plan by latency (a few dependent reads and cluster barriers; the pool is read
+// once), the copies and compact by memory bandwidth.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -34,13 +34,23 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxCtas = 8;            // portable cluster size
 constexpr int kPagesThreads = 256;
 
+// What the cluster of the plan does itself: at most this many page pieces of kCopyPiece bytes to
+// copy and runs of 128 table entries to go through, eight rounds of its 256 warps (a second
+// launch costs more up to there), in at most kFusedLayers layers (a small kernel argument).
+constexpr int kFusedChunks = 2048;
+constexpr int kCopyPiece = 2048;
+constexpr int kFusedLayers = 8;
+
 // The pools that a call moves slots in (one per model layer).
-struct PageLayers {
+template <int N>
+struct PageLayersOf {
   int32_t count;
-  uint8_t* base[kMaxPageLayers];
-  int64_t blk_stride[kMaxPageLayers];      // bytes between pages
-  int32_t page_bytes[kMaxPageLayers];      // a multiple of 128
+  uint8_t* base[N];
+  int64_t blk_stride[N];                   // bytes between pages
+  int32_t page_bytes[N];                   // a multiple of 128
 };
+using PageLayers = PageLayersOf<kMaxPageLayers>;
+using FewLayers = PageLayersOf<kFusedLayers>;
 
 struct PlanParams {
   int32_t* table;                          // [batch, cols]
@@ -106,6 +116,20 @@ __device__ __forceinline__ int last_not_above(const unsigned* a, int n, unsigned
   return lo;
 }
 
+// The position of the n-th set bit (from 0) of w.
+__device__ __forceinline__ int nth_bit(uint32_t w, int n) {
+  int at = 0;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const int c = __popc((w >> at) & ((1u << s) - 1u));
+    if (n >= c) {
+      n -= c;
+      at += s;
+    }
+  }
+  return at;
+}
+
 __host__ __device__ __forceinline__ int pages_of(int tokens) {
   return tokens / kPageTokens + (tokens % kPageTokens != 0);
 }
@@ -155,8 +179,71 @@ __device__ __forceinline__ Demand fork_demand(const PlanParams& p, int i, const 
   return d;
 }
 
-template <bool FORK>
-__global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PlanParams p) {
+// Entries c0 + t, c0 + t + n, ... (four of them, below the sequence's pages) of sequence b that
+// a resize from len to want tokens releases: those past the new length, and with a window those
+// whose tokens no query at a position >= min(len, want) sees.
+__device__ __forceinline__ void release_entries(const PlanParams& p, int b, int len, int want, int c0,
+                                                int n, int t) {
+  const int have = pages_of(len), keep = pages_of(want), least = min(len, want);
+  // all tokens >= sinks and < least - window + 1
+  const int w0 = p.window > 0 ? pages_of(p.sinks) : 0;
+  const int w1 = p.window > 0 ? max(0, least - p.window + 1) / kPageTokens : 0;
+  int32_t* row = p.table + b * p.table_stride;
+  int32_t id[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = c0 + t + j * n;
+    id[j] = c < have && (c >= keep || (c >= w0 && c < w1)) ? row[c] : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (id[j] < 0) continue;
+    if (id[j] < p.pool) atomicSub(&p.refs[id[j]], 1);
+    else report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
+    row[c0 + t + j * n] = -1;
+  }
+}
+
+// Entries c0 + t, c0 + t + n, ... (four of them, below `end`) of the parent's row to the child's,
+// their pages shared.
+__device__ __forceinline__ void share_entries(const PlanParams& p, int parent, int child, int end, int c0,
+                                              int n, int t) {
+  const int32_t* src = p.table + parent * p.table_stride;
+  int32_t* dst = p.table + child * p.table_stride;
+  int32_t id[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) id[j] = c0 + t + j * n < end ? src[c0 + t + j * n] : -1;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (c0 + t + j * n >= end) continue;
+    dst[c0 + t + j * n] = id[j];
+    if (id[j] < 0) continue;
+    if (id[j] < p.pool) atomicAdd(&p.refs[id[j]], 1);
+    else report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
+  }
+}
+
+// 16-byte units [u0, u1) of a page, by n threads, four loads in flight each.
+template <class Layers>
+__device__ __forceinline__ void copy_units(const Layers& l, int layer, int from, int to, int u0, int u1,
+                                           int n, int t) {
+  const uint4* s = (const uint4*)(l.base[layer] + from * l.blk_stride[layer]);
+  uint4* d = (uint4*)(l.base[layer] + to * l.blk_stride[layer]);
+  for (int i0 = u0 + t; i0 < u1; i0 += 4 * n) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * n < u1) v[j] = s[i0 + j * n];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * n < u1) d[i0 + j * n] = v[j];
+  }
+}
+
+// FUSED: the cluster also does what the second launch does otherwise.
+template <bool FORK, bool FUSED>
+__global__ void __launch_bounds__(kPlanThreads, 1)
+pages_plan_kernel(const PlanParams p, const __grid_constant__ FewLayers layers, int pieces) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -231,7 +318,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PlanP
     const int i = last_not_above(need, p.requests + 1, r);
     if (need[i + 1] > free_pages) continue;          // refused as a whole
     const int w = last_not_above(before, words + 1, r - first);
-    const int page = (word0 + w) * 32 + (int)__fns(bitmap[w], 0, (int)(r - first - before[w]) + 1);
+    const int page = (word0 + w) * 32 + nth_bit(bitmap[w], (int)(r - first - before[w]));
     const int k = (int)(r - need[i]);
     p.refs[page] = 1;
     const int seq = FORK ? p.children[i] : i;
@@ -263,22 +350,43 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PlanP
     }
   }
   cluster.sync();        // no CTA leaves while another may read its total
+  if constexpr (FUSED) {
+    const int warp = rank * (kPlanThreads / 32) + (tid >> 5), warps = ctas * (kPlanThreads / 32);
+    auto served = [&](int i) {
+      return !(kind[i] & kBadRequest) && !((kind[i] & kAsksPages) && need[i + 1] > free_pages);
+    };
+    const int runs = (p.cols + 127) / 128;
+    for (int item = warp; item < p.requests * runs; item += warps) {
+      const int i = item / runs, c0 = (item - i * runs) * 128;
+      if (c0 >= pages_of(lens[i]) || !served(i)) continue;
+      if (FORK) {
+        // a partly filled last page without a copy is a hole (or out of range) in the parent too
+        const int end = (kind[i] & kAsksCopy) ? lens[i] / kPageTokens : pages_of(lens[i]);
+        share_entries(p, p.parents[i], p.children[i], end, c0, 32, lane);
+      } else {
+        release_entries(p, i, lens[i], p.new_lens[i], c0, 32, lane);
+      }
+    }
+    for (int item = warp; item < p.requests * layers.count * pieces; item += warps) {
+      const int i = item / (layers.count * pieces), rest = item - i * layers.count * pieces;
+      const int layer = rest / pieces, piece = rest - layer * pieces;
+      if (!(kind[i] & kAsksCopy) || !served(i)) continue;
+      const int units = layers.page_bytes[layer] / 16, u0 = piece * (kCopyPiece / 16);
+      copy_units(layers, layer, p.moves[2 * i], p.moves[2 * i + 1], u0, min(units, u0 + kCopyPiece / 16), 32,
+                 lane);
+    }
+    if (!FORK && rank == 0) {                // every CTA read the old lengths before the barrier
+      for (int i = tid; i < p.requests; i += kPlanThreads) {
+        if (!served(i)) continue;
+        if (kind[i] & kAsksCopy) atomicSub(&p.refs[p.moves[2 * i]], 1);
+        p.seq_lens[i] = p.new_lens[i];
+      }
+    }
+  }
 }
 
-// 16-byte units [0, bytes) of one page copied by the block, four loads in flight a thread.
 __device__ __forceinline__ void copy_page(const PageLayers& l, int layer, int from, int to) {
-  const uint4* s = (const uint4*)(l.base[layer] + from * l.blk_stride[layer]);
-  uint4* d = (uint4*)(l.base[layer] + to * l.blk_stride[layer]);
-  const int n = l.page_bytes[layer] / 16;
-  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kPagesThreads) {
-    uint4 v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i0 + j * kPagesThreads < n) v[j] = s[i0 + j * kPagesThreads];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i0 + j * kPagesThreads < n) d[i0 + j * kPagesThreads] = v[j];
-  }
+  copy_units(l, layer, from, to, 0, l.page_bytes[layer] / 16, kPagesThreads, threadIdx.x);
 }
 
 // Second launch of resize: grid (batch, 1 + layers).  CTA (b, 0) releases sequence b's
@@ -293,20 +401,8 @@ pages_resize_kernel(const PlanParams p, const __grid_constant__ PageLayers layer
     return;
   }
   const int len = p.seq_lens[b], want = p.new_lens[b];
-  const int have = pages_of(len), keep = pages_of(want), least = min(len, want);
-  int32_t* row = p.table + b * p.table_stride;
-  // pages no query at a position >= least sees: all tokens >= sinks and < least - window + 1
-  const int w0 = p.window > 0 ? pages_of(p.sinks) : 0;
-  const int w1 = p.window > 0 ? max(0, least - p.window + 1) / kPageTokens : 0;
-  auto release = [&](int c) {
-    const int id = row[c];
-    if (id < 0) return;
-    if (id < p.pool) atomicSub(&p.refs[id], 1);
-    else report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
-    row[c] = -1;
-  };
-  for (int c = w0 + threadIdx.x; c < min(w1, min(have, keep)); c += kPagesThreads) release(c);
-  for (int c = keep + threadIdx.x; c < have; c += kPagesThreads) release(c);
+  for (int c0 = 0; c0 < pages_of(len); c0 += 4 * kPagesThreads)
+    release_entries(p, b, len, want, c0, kPagesThreads, threadIdx.x);
   __syncthreads();                         // the old length has been read
   if (threadIdx.x == 0) {
     if (from >= 0) atomicSub(&p.refs[from], 1);
@@ -329,22 +425,9 @@ pages_fork_kernel(const PlanParams p, const __grid_constant__ PageLayers layers,
   }
   const int child = p.children[i];
   const int len = p.seq_lens[child];       // the parent's before the call
-  const int32_t* src = p.table + p.parents[i] * p.table_stride;
-  int32_t* dst = p.table + child * p.table_stride;
   // a partly filled last page without a copy is a hole (or out of range) in the parent too
   const int end = from >= 0 ? len / kPageTokens : pages_of(len);
-  const int c0 = blockIdx.y * kForkChunk;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = c0 + j * kPagesThreads + threadIdx.x;
-    if (c >= end) break;
-    const int id = src[c];
-    dst[c] = id;
-    if (id >= 0) {
-      if (id < p.pool) atomicAdd(&p.refs[id], 1);
-      else report_error(p.err, TQ_DEVERR_BLOCK_RANGE);
-    }
-  }
+  share_entries(p, p.parents[i], child, end, blockIdx.y * kForkChunk, kPagesThreads, threadIdx.x);
 }
 
 struct CompactParams {
@@ -366,9 +449,9 @@ struct CompactParams {
 // Rows [0, counts[b]) of sequence b in the destination pages <- its rows positions[b, .].
 // One CTA per destination page, sequence and layer: its 16 rows' addresses are resolved
 // once, then their U-byte units are copied with four loads in flight a thread.
-template <typename U>
+template <typename U, class Layers>
 __global__ void __launch_bounds__(kPagesThreads)
-pages_compact_kernel(const CompactParams p, const __grid_constant__ PageLayers layers) {
+pages_compact_kernel(const CompactParams p, const __grid_constant__ Layers layers) {
   const int b = blockIdx.y, layer = blockIdx.z;
   const int count = p.counts[b], len = p.src_lens[b];
   if (count < 0 || count > p.max_keep || pages_of(count) > p.dst_cols || len < 0 ||
