@@ -41,6 +41,7 @@ struct AttendParams {
   int32_t k_region;             // bytes of the K region (offset of the V region)
   int32_t window, sinks;
   int32_t tile_rows;            // rows a CTA of the tiles kernel takes
+  int32_t row_tiles;            // row tiles of the longest chunk
   unsigned int* err;
   uint32_t wait_ms;
 };
@@ -50,6 +51,34 @@ struct AttendSeq {
   int32_t row0, n_q, len;
   bool skip;                    // a bad row range: nothing is written
 };
+
+// What a cluster works on.  The grid is one dimension of clusters: KV heads, then row tiles
+// (the last first: it sees most keys), then sequences, the longest first where that pays (RANK)
+// and a warp can rank them, so that what takes longest starts first.
+struct AttendItem {
+  int b, kvh, tile;
+};
+template <bool RANK>
+__device__ __forceinline__ AttendItem attend_item(const AttendParams& p, int ctas) {
+  const int lane = threadIdx.x & 31;
+  int i = blockIdx.x / ctas;
+  AttendItem it;
+  it.kvh = i % p.h_kv;
+  i /= p.h_kv;
+  it.tile = p.row_tiles - 1 - i % p.row_tiles;
+  it.b = i / p.row_tiles;
+  if (RANK && p.batch > 1 && p.batch <= 32) {
+    const int len = lane < p.batch ? p.seq_lens[lane] : -1;
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < p.batch; ++j) {
+      const int other = __shfl_sync(0xffffffffu, len, j);
+      rank += other > len || (other == len && j < lane);
+    }
+    it.b = __ffs(__ballot_sync(0xffffffffu, lane < p.batch && rank == it.b)) - 1;
+  }
+  return it;
+}
 
 __device__ __forceinline__ AttendSeq attend_seq(const AttendParams& p, int b, bool report) {
   AttendSeq s;

@@ -19,10 +19,13 @@ constexpr int kRowsMost = 32;
 // times a CTA's time are least; alone and joined are the times of a CTA's start and end in
 // units of keys, without and with a join.
 template <auto kern>
-tq_status launch_attend(const AttendParams& p, int64_t tiles, int threads, int smem, int64_t units,
+tq_status launch_attend(AttendParams p, int64_t tiles, int threads, int smem, int64_t units,
                         int alone, int joined, int least, cudaStream_t st) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
+  const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
+  if (groups > 0x7fffffff / 8) return TQ_ERR_UNSUPPORTED;
+  p.row_tiles = (int32_t)tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
@@ -34,11 +37,10 @@ tq_status launch_attend(const AttendParams& p, int64_t tiles, int threads, int s
   cfg.numAttrs = 1;
   auto grid = [&](int ctas) {
     attr[0].val.clusterDim.x = (unsigned)ctas;
-    cfg.gridDim = dim3((unsigned)(p.batch * ctas), (unsigned)p.h_kv, (unsigned)tiles);
+    cfg.gridDim = dim3((unsigned)(groups * ctas));
   };
   // clusters of each size that the GPU holds at once (a property of the kernel)
   static std::atomic<int> fit[4];
-  const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
   int best = 1;
   int64_t best_cost = 0;
   for (int i = 0; i < 4; ++i) {

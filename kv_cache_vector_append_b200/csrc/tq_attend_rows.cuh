@@ -143,11 +143,12 @@ attend_rows_kernel(const AttendParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int ctas = (int)cluster.num_blocks(), split = (int)cluster.block_rank();
-  const int b = blockIdx.x / ctas, kvh = blockIdx.y, G = p.group;
+  const AttendItem item = attend_item<false>(p, ctas);
+  const int b = item.b, kvh = item.kvh, G = p.group;
 
-  const AttendSeq sq = attend_seq(p, b, tid == 0 && split == 0 && kvh == 0 && blockIdx.z == 0);
+  const AttendSeq sq = attend_seq(p, b, tid == 0 && split == 0 && kvh == 0 && item.tile == 0);
   // this cluster's rows [r0, r0 + rows) of the KV head's n_q * G
-  const int r0 = blockIdx.z * ROWS;
+  const int r0 = item.tile * ROWS;
   const int rows = min(ROWS, sq.n_q * G - r0);
   if (rows <= 0) return;                    // the whole cluster
   const int p0 = sq.len - sq.n_q;           // position of row 0

@@ -361,12 +361,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   float* part_s = (float*)smem;                          // [slot][row][PART], at the end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = (int)cluster.num_blocks(), split = (int)cluster.block_rank();
-  const int b = blockIdx.x / ctas, kvh = blockIdx.y, G = p.group;
+  const AttendItem item = attend_item<true>(p, ctas);
+  const int b = item.b, kvh = item.kvh, G = p.group;
 
-  const AttendSeq sq = attend_seq(p, b, tid == 0 && split == 0 && kvh == 0 && blockIdx.z == 0);
-  // later rows see more keys: they start first
+  const AttendSeq sq = attend_seq(p, b, tid == 0 && split == 0 && kvh == 0 && item.tile == 0);
   const int tile_rows = p.tile_rows;                     // kTileRows, or twice that (kTwoTiles)
-  const int r0 = ((int)gridDim.z - 1 - (int)blockIdx.z) * tile_rows;
+  const int r0 = item.tile * tile_rows;
   const int rows = min(tile_rows, sq.n_q * G - r0);
   if (rows <= 0) return;                                 // the whole cluster
   const int p0 = sq.len - sq.n_q;

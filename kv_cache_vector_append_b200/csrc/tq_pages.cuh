@@ -7,9 +7,8 @@
 //
 // resize and fork plan and allocate in one cluster: it turns the counts into a bitmap of free
 // pages in shared memory (each CTA a contiguous part of the pool), joins the CTAs' totals over
-// distributed shared memory, and lets thread r of the demanded ranks find its page (a search
-// in the prefix sums of the bitmap's words, then the n-th set bit) and its request (a search
-// in the prefix sums of the demands).  What follows is long: page copies, shared or released
+// distributed shared memory, and lets every free page find its rank (prefix sums of the
+// bitmap's words) and the request of that rank (a search in the prefix sums of the demands).  What follows is long: page copies, shared or released
 // table entries, count updates (integer atomics, so their order does not matter).  Where it is
 // little (see kFusedChunks) the cluster's warps do it themselves after a cluster barrier, else
 // a second launch with a CTA per sequence and layer.  What that needs to know of the plan is
@@ -35,9 +34,9 @@ constexpr int kPlanMaxCtas = 8;            // portable cluster size
 constexpr int kPagesThreads = 256;
 
 // What the cluster of the plan does itself: at most this many page pieces of kCopyPiece bytes to
-// copy and runs of 128 table entries to go through, eight rounds of its 256 warps (a second
+// copy and runs of 128 table entries to go through, four rounds of its 256 warps (a second
 // launch costs more up to there), in at most kFusedLayers layers (a small kernel argument).
-constexpr int kFusedChunks = 2048;
+constexpr int kFusedChunks = 1024;
 constexpr int kCopyPiece = 2048;
 constexpr int kFusedLayers = 8;
 
@@ -114,20 +113,6 @@ __device__ __forceinline__ int last_not_above(const unsigned* a, int n, unsigned
     else hi = mid;
   }
   return lo;
-}
-
-// The position of the n-th set bit (from 0) of w.
-__device__ __forceinline__ int nth_bit(uint32_t w, int n) {
-  int at = 0;
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    const int c = __popc((w >> at) & ((1u << s) - 1u));
-    if (n >= c) {
-      n -= c;
-      at += s;
-    }
-  }
-  return at;
 }
 
 __host__ __device__ __forceinline__ int pages_of(int tokens) {
@@ -260,11 +245,21 @@ pages_plan_kernel(const PlanParams p, const __grid_constant__ FewLayers layers, 
   const int tid = threadIdx.x, lane = tid & 31;
   const int word0 = rank * words;
 
-  // free pages of this part: one ballot a word
-  for (int w = tid >> 5; w < words; w += kPlanThreads / 32) {
-    const int64_t page = (int64_t)(word0 + w) * 32 + lane;
-    const uint32_t bits = __ballot_sync(0xffffffffu, page < p.pool && p.refs[page] == 0);
-    if (lane == 0) bitmap[w] = bits;
+  // free pages of this part: one ballot a word, eight words' counts in flight
+  for (int w0 = tid >> 5; w0 < words; w0 += 8 * (kPlanThreads / 32)) {
+    int n[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int w = w0 + j * (kPlanThreads / 32);
+      const int64_t page = (int64_t)(word0 + w) * 32 + lane;
+      n[j] = w < words && page < p.pool ? p.refs[page] : 1;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int w = w0 + j * (kPlanThreads / 32);
+      const uint32_t bits = __ballot_sync(0xffffffffu, n[j] == 0);
+      if (lane == 0 && w < words) bitmap[w] = bits;
+    }
   }
   if (FORK) {
     for (int b = tid; b < p.batch; b += kPlanThreads) owner[b] = 0x7fffffff;
@@ -312,13 +307,16 @@ pages_plan_kernel(const PlanParams p, const __grid_constant__ FewLayers layers, 
     if (c < rank) first += n;
     free_pages += n;
   }
-  // the ranks [first, first + carry) of the demand are served from this part
-  const unsigned end = min(first + carry, asked);
-  for (unsigned r = first + tid; r < end; r += kPlanThreads) {
+  // the ranks [first, first + carry) of the demand are served from this part: a warp takes a
+  // word of the bitmap, a lane a page of it
+  for (int w = tid >> 5; w < words; w += kPlanThreads / 32) {
+    if (first + before[w] >= asked) break;
+    const uint32_t bits = bitmap[w];
+    const unsigned r = first + before[w] + __popc(bits & ((1u << lane) - 1u));
+    if (!((bits >> lane) & 1u) || r >= asked) continue;
     const int i = last_not_above(need, p.requests + 1, r);
     if (need[i + 1] > free_pages) continue;          // refused as a whole
-    const int w = last_not_above(before, words + 1, r - first);
-    const int page = (word0 + w) * 32 + nth_bit(bitmap[w], (int)(r - first - before[w]));
+    const int page = (word0 + w) * 32 + lane;
     const int k = (int)(r - need[i]);
     p.refs[page] = 1;
     const int seq = FORK ? p.children[i] : i;
