@@ -50,10 +50,10 @@ class Case:
                           self.pages.cpu().numpy(), self.table.cpu().numpy(), self.lens.cpu().numpy(), s.head_dim,
                           s.k_bits, s.v_bits, SEED, self.scale, window, sinks, out_eps(self.out.dtype))
 
-    def check(self, window=0, sinks=0):
+    def check(self, window=0, sinks=0, together=False):
         got = to_np_f64(self.run(window, sinks))
         torch.cuda.synchronize()
-        return check_rows(got, *self.ref(window, sinks))
+        return check_rows(got, *self.ref(window, sinks), out_eps(self.out.dtype) if together else None)
 
 
 # lengths around the page and tile borders, new tokens from none to all of the sequence
@@ -76,13 +76,21 @@ GEOMETRIES = [
     (64, 14, 2, 8, 8, [700, 100], [33, 100], 128, 20, "bf16"),
     (256, 4, 2, 3, 4, [420], [150], 33, 17, "bf16"),
     (128, 4, 1, 4, 4, [900], [260], 150, 200, "bf16"),
+    # keys split over several blocks: one and two row tiles, few rows, odd ends
+    (128, 8, 2, 4, 4, [5001, 2100], [20, 41], 0, 0, "bf16"),
+    (128, 8, 2, 3, 2, [4100], [200], 0, 0, "f16"),
+    (128, 8, 2, 8, 8, [3333], [130], 2000, 5, "bf16"),
+    (64, 14, 2, 8, 8, [3500, 77], [11, 60], 0, 0, "bf16"),
+    (256, 4, 2, 4, 3, [2600], [50], 0, 0, "bf16"),
+    (128, 8, 2, 4, 2, [3000, 4000], [8, 3], 0, 0, "f32"),
+    (256, 4, 2, 8, 2, [2000], [3], 0, 0, "f16"),
 ]
 
 
 @pytest.mark.parametrize("d,hq,hkv,kb,vb,lens,q_lens,window,sinks,dtype", GEOMETRIES)
 def test_attend_against_the_definition(d, hq, hkv, kb, vb, lens, q_lens, window, sinks, dtype):
     tq = _tq()
-    Case(tq, d, hq, hkv, kb, vb, lens, q_lens, dtype).check(window, sinks)
+    Case(tq, d, hq, hkv, kb, vb, lens, q_lens, dtype).check(window, sinks, together=True)
     assert tq.get_device_error() == 0
 
 
@@ -103,7 +111,7 @@ def test_decode_window_against_the_definition(d, hq, hkv, kb, vb, window, sinks)
     lens = [1, 63, 64, 65, 0, 1100, 333]
     c = Case(tq, d, hq, hkv, kb, vb, lens, [1] * len(lens))
     tq.paged_decode_window(c.out, c.q, c.pages, c.table, c.lens, c.cb, SEED, c.scale, window, sinks)
-    check_rows(to_np_f64(c.out), *c.ref(window, sinks))
+    check_rows(to_np_f64(c.out), *c.ref(window, sinks), out_eps(c.out.dtype))
     # the same as a chunk of one token each
     one = c.out.clone()
     assert torch.equal(one, c.run(window, sinks))
@@ -195,6 +203,47 @@ def test_unseen_tokens_may_hold_anything(q_lens, window, sinks):
     c.table = torch.from_numpy(table).cuda()
     c.check(window, sinks)
     assert tq.get_device_error() == 0
+
+
+@pytest.mark.parametrize("n,longest,q_len", [(170, 5000, 1), (40, 5000, 70), (20, 2500, 70), (40, 700, 6)])
+def test_many_sequences(n, longest, q_len):
+    """More and fewer sequences than a warp ranks, one of them far longer than the others."""
+    tq = _tq()
+    rng = np.random.default_rng(n)
+    lens = rng.integers(1, 90, n)
+    lens[n // 3] = longest
+    q_lens = np.minimum(rng.integers(0, 4, n), lens)
+    q_lens[n // 3], q_lens[0] = q_len, min(q_len, lens[0])
+    c = Case(tq, 128, 8, 2, 4, 2, lens.tolist(), q_lens.tolist())
+    c.check()
+    c.check(300, 3)
+    assert tq.get_device_error() == 0
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [7, 3], [90, 40]])
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1e-30])
+def test_scales_of_either_sign(q_lens, scale):
+    tq = _tq()
+    c = Case(tq, 128, 8, 2, 4, 4, [300, 100], q_lens)
+    c.scale = scale
+    c.check()
+    c.check(50, 3)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [7, 3], [90, 40]])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_at_odd_addresses(q_lens, dtype):
+    """q and out whose rows start on no 16-byte boundary, both as q's type and as f32."""
+    tq = _tq()
+    c = Case(tq, 128, 8, 2, 4, 4, [300, 100], q_lens, dtype)
+    want = c.run().clone()
+    n = c.q.shape[0]
+    q = torch.zeros(n, 8, 133, dtype=c.q.dtype, device="cuda")[:, :, 3:131]
+    q.copy_(c.q)
+    for out_dtype in (c.q.dtype, torch.float32):
+        out = torch.zeros(n, 8, 131, dtype=out_dtype, device="cuda")[:, :, 1:129]
+        tq.paged_attend(out, q, c.starts, c.pages, c.table, c.lens, c.cb, SEED, c.scale, c.max_q)
+        assert torch.equal(out.to(c.q.dtype), want)
 
 
 @pytest.mark.parametrize("rows", [1, 3, 40])
