@@ -63,7 +63,7 @@ struct TilesCfg {
   // in the place of the second row tile's q
   static constexpr int NBUF = kOneO ? 4 : 2;
   static constexpr int NORMS = NBUF * N * 2 * 4;
-  static constexpr int MISC = 640;
+  static constexpr int MISC = 1024;
   // more than half an SM: a CTA that holds all of tensor memory has the SM to itself
   static constexpr int RAW = OPER + LUT + NORMS + MISC;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
@@ -89,6 +89,7 @@ struct TileInfo {
 };
 
 struct TilesMisc {
+  uint4 flip[32];                          // sign bits of the coordinates, as in a 16-bit row
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2], norm_full[4], ring_full[3], ring_empty[3], o_done, q_ready;
   unsigned long long best;
   float alpha;
@@ -97,7 +98,7 @@ struct TilesMisc {
   TileMeta meta[2][kDequantWarps];
   TileInfo info[4];
 };
-static_assert(sizeof(TilesMisc) <= 640, "misc area");
+static_assert(sizeof(TilesMisc) <= 1024, "misc area");
 
 __device__ __forceinline__ void umma_ts_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -266,19 +267,17 @@ __device__ __forceinline__ void group_fwht(float (&x)[16], int l) {
       x[i] = (l & m) ? o - x[i] : x[i] + o;
     }
 }
-// The signs of the coordinates that a lane holds, a bit each.
+// The signs of the coordinates that a lane holds (flip: sign bits in pairs of 16-bit fields).
 template <int D>
-__device__ __forceinline__ uint32_t group_signs(uint64_t seed, int l) {
-  uint32_t s = 0u;
+__device__ __forceinline__ void group_flip(float (&x)[16], const uint4* flip, int l) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    s |= (sign_mask_at(seed, group_coord<D>(l, i / 4) + i % 4) >> 31) << i;
-  return s;
-}
-__device__ __forceinline__ void group_flip(float (&x)[16], uint32_t signs) {
+  for (int j = 0; j < 4; ++j) {
+    const uint2 f = ((const uint2*)flip)[group_coord<D>(l, j) / 4];
+    const uint32_t m[4] = {f.x << 16, f.x, f.y << 16, f.y};
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((signs << (31 - i)) & 0x80000000u));
+    for (int e = 0; e < 4; ++e)
+      x[4 * j + e] = __uint_as_float(__float_as_uint(x[4 * j + e]) ^ (m[e] & 0x80000000u));
+  }
 }
 // Its elements from / to memory; vec: rows start on 16-byte boundaries.
 template <int D>
@@ -323,6 +322,28 @@ __device__ __forceinline__ void group_store(const float (&x)[16], void* base, in
       for (int e = 0; e < 4; ++e) store_from_f32(base, at + e, dtype, x[4 * j + e]);
     }
   }
+}
+
+// FWHT over C consecutive values of a thread (natural order, no scaling).
+template <int C>
+__device__ __forceinline__ void thread_fwht(float* x) {
+#pragma unroll
+  for (int i = 0; i < C; i += 2) {
+    const float a = x[i], b = x[i + 1];
+    x[i] = a + b;
+    x[i + 1] = a - b;
+  }
+  const float2 neg = make_float2(-1.0f, -1.0f);
+#pragma unroll
+  for (int h = 2; h < C; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < C; i += 2)
+      if ((i & h) == 0) {
+        const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[i + h], x[i + h + 1]);
+        const float2 u = add2(a, b), v = fma2(b, neg, a);
+        x[i] = u.x, x[i + 1] = u.y;
+        x[i + h] = v.x, x[i + h + 1] = v.y;
+      }
 }
 
 // mbar_wait for waits that are usually short: some polls before the clock is read.
@@ -407,6 +428,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     fence_mbar_init();
   }
   if (warp == 12) tmem_alloc(&ms->tmem, 512);
+  if (warp == 13)
+    for (int i = lane; i < D / 2; i += 32)
+      ((uint32_t*)ms->flip)[i] = (sign_mask_at(p.sign_seed, 2 * i) >> 16) | sign_mask_at(p.sign_seed, 2 * i + 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -420,7 +444,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   // into the operand; its scale to qs_s
   auto make_q = [&](int w, int warps) {
     const int l = lane % C::LPR;
-    const uint32_t signs = group_signs<D>(p.sign_seed, l);
     const int all = two ? 2 * kTileRows : kTileRows;
     auto load = [&](float (&x)[16], int r) {
       const int t = (r0 + r) / G, g = r0 + r - t * G;
@@ -439,7 +462,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = next[i];
       load(next, rb + warps * C::RPI < all ? r + warps * C::RPI : rows);
-      group_flip(x, signs);
+      group_flip<D>(x, ms->flip, l);
       group_fwht<D>(x, l);
       float ss = 0.f;
 #pragma unroll
@@ -455,6 +478,38 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         *(uint2*)(qt + at) = make_uint2(pack_half2(a, b), pack_half2(c, d));
       }
       if (l == 0) qs_s[r] = nrm * inv_sqrt_dim<D>() * fabsf(p.scale_log2);
+    }
+  };
+  // 16-bit rows instead come as they are, 16 bytes a lane, into the operand's place, where a
+  // thread then turns each row into q' (without shuffles; a CTA's start 20 to 16 thousand clocks)
+  const bool raw_q = !C::kOneO && p.q_dtype != TQ_F32;
+  auto load_q = [&](int w, int warps) {
+    constexpr int CH = D / 8;                            // 16-byte pieces of a row
+    const int all = (two ? 2 * kTileRows : kTileRows) * CH, step = warps * 32, i0 = w * 32 + lane;
+#pragma unroll 1
+    for (int i = i0; i < all; i += 4 * step) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = (i + j * step) / CH, c = (i + j * step) % CH;
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const int t = (r0 + r) / G, g = r0 + r - t * G;
+          const uint16_t* at = (const uint16_t*)p.q + (int64_t)(sq.row0 + t) * p.q_rstride +
+                               (int64_t)(kvh * G + g) * p.q_hstride + 8 * c;
+          if (p.q_vec)
+            v[j] = *(const uint4*)at;
+          else
+            v[j] = make_uint4(at[0] | (uint32_t)at[1] << 16, at[2] | (uint32_t)at[3] << 16,
+                              at[4] | (uint32_t)at[5] << 16, at[6] | (uint32_t)at[7] << 16);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = (i + j * step) / CH, c = (i + j * step) % CH;
+        if (i + j * step < all)
+          *(uint4*)(q_s + r / kTileRows * C::QTILE + sw128_offset(r % kTileRows, 8 * c, kTileRows)) = v[j];
+      }
     }
   };
   if constexpr (C::kOneO) {
@@ -483,7 +538,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   if (warp >= 12) {
     regs_dec<kIssueRegs>();
     if constexpr (!C::kOneO) {
-      make_q(warp - 4, 12);
+      if (raw_q) load_q(warp - 4, 12);
+      else make_q(warp - 4, 12);
       fence_proxy_async_smem();                          // q is read by the tensor cores
       asm volatile("bar.sync 2, 384;" ::: "memory");
     }
@@ -810,8 +866,59 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     regs_inc<kSoftmaxRegs>();
     const int slot = warp >> 2;
     if constexpr (!C::kOneO) {
-      make_q(warp, 12);
-      asm volatile("bar.sync 2, 384;" ::: "memory");     // the warps that made q
+      if (raw_q) {
+        load_q(warp, 12);
+        asm volatile("bar.sync 2, 384;" ::: "memory");   // the warps that loaded q
+        if (two || slot == 0) {
+          // q' of this thread's row, in place: sign flips, FWHT, 1/sqrt(D), to unit length in fp16
+          uint8_t* qt = q_s + (two ? slot : 0) * C::QTILE;
+          float x[D];
+#pragma unroll
+          for (int c = 0; c < D; c += 8) {
+            const uint4 v = *(const uint4*)(qt + sw128_offset(srow, c, kTileRows));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint4 f = ms->flip[c / 8];
+            const uint32_t m[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t u = w[i] ^ m[i];
+              if (p.q_dtype == TQ_BF16) {
+                x[c + 2 * i] = __uint_as_float(u << 16);
+                x[c + 2 * i + 1] = __uint_as_float(u & 0xffff0000u);
+              } else {
+                const float2 h = __half22float2(*(const __half2*)&u);
+                x[c + 2 * i] = h.x;
+                x[c + 2 * i + 1] = h.y;
+              }
+            }
+          }
+          thread_fwht<D>(x);
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < D; i += 2) {
+            const float2 v = make_float2(x[i], x[i + 1]);
+            s2[i / 2 % 2] = fma2(v, v, s2[i / 2 % 2]);
+          }
+          const float nrm = sqrtf((s2[0].x + s2[1].x) + (s2[0].y + s2[1].y));
+          const float inv = nrm > 0.f ? copysignf(1.0f / nrm, p.scale_log2) : 0.f;
+          const float2 i2 = make_float2(inv, inv);
+#pragma unroll
+          for (int c = 0; c < D; c += 8) {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 v = mul2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), i2);
+              h[i] = pack_half2(v.x, v.y);
+            }
+            *(uint4*)(qt + sw128_offset(srow, c, kTileRows)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          qs_s[myrow] = nrm * inv_sqrt_dim<D>() * fabsf(p.scale_log2);
+        }
+        asm volatile("bar.sync 3, 256;" ::: "memory");   // the softmax warps
+      } else {
+        make_q(warp, 12);
+        asm volatile("bar.sync 2, 384;" ::: "memory");   // the warps that made q
+      }
       qs = qs_s[myrow];
       fence_proxy_async_smem();                          // q is read by the tensor cores
       __syncwarp();
@@ -964,19 +1071,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     tc_fence_after();
     if (!(C::kOneO && slot)) {
       float* rec = part_s + (slot * kTileRows + srow) * PART;
+      // the stages of the inverse rotation inside a quarter of the row go here, before the join
+      // (which is linear), the two others after it
+      constexpr int Q = D / 4;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
+      for (int c = 0; c < D; c += Q) {
+        float o[Q];
         if (items > 0 && ok) {
-          tmem_ld16_nowait(o_at + c, o);
-          tmem_ld16_nowait(o_at + c + 16, o + 16);
+#pragma unroll
+          for (int i = 0; i < Q; i += 16) tmem_ld16_nowait(o_at + c + i, o + i);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          for (int i = 0; i < Q; ++i) o[i] = 0.f;
         }
+        thread_fwht<Q>(o);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) *(float4*)(rec + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        for (int i = 0; i < Q; i += 4) *(float4*)(rec + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
       // a sum that is not a number must survive the join, which drops empty partials
       rec[D] = sum != sum && M == -INFINITY ? -3e38f : M;
@@ -990,7 +1101,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   if (ctas > 1) cluster.sync();
   // row r is joined by CTA r % ctas of the cluster, by a group of lanes; records: CTAs x slots
   const int recs = two || C::kOneO ? 1 : 2, l = lane % C::LPR;
-  const uint32_t signs = group_signs<D>(p.sign_seed, l);
 #pragma unroll 1
   for (int rb = warp * C::RPI; rb * ctas < rows; rb += kTilesWarps * C::RPI) {
     const int r = (rb + lane / C::LPR) * ctas + split, t = (r0 + r) / G, g = r0 + r - t * G;
@@ -1002,12 +1112,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         const float* from = part_s + ((recs == 2 ? (i & 1) * kTileRows : 0) + r) * PART;
         return ctas > 1 ? cluster.map_shared_rank(from, recs == 2 ? i >> 1 : i) : from;
       };
+      if (ctas * recs > 1) {
 #pragma unroll 1
-      for (int i = 0; i < ctas * recs; ++i) top = fmaxf(top, record(i)[D]);
+        for (int i = 0; i < ctas * recs; ++i) top = fmaxf(top, record(i)[D]);
+      }
 #pragma unroll 1
       for (int i = 0; i < ctas * recs; ++i) {
         const float* from = record(i);
-        const float m = from[D], w = m == -INFINITY ? 0.f : exp2f(m - top);
+        const float m = from[D], w = ctas * recs == 1 ? 1.0f : m == -INFINITY ? 0.f : exp2f(m - top);
         sum = fmaf(w, from[D + 1], sum);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1022,8 +1134,16 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     const float inv = sum == 0.f ? 0.f : inv_sqrt_dim<D>() / sum;   // a row that sees nothing: 0
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] *= inv;
-    group_fwht<D>(o, l);
-    group_flip(o, signs);
+#pragma unroll
+    for (int h = 4; h < 16; h <<= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((i & h) == 0) {
+          const float a = o[i], c = o[i + h];
+          o[i] = a + c;
+          o[i + h] = a - c;
+        }
+    group_flip<D>(o, ms->flip, l);
     if (r < rows)
       group_store<D>(o, p.out, (int64_t)(sq.row0 + t) * p.o_rstride + (int64_t)(kvh * G + g) * p.o_hstride,
                      p.out_dtype, p.out_vec, l);
