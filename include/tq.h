@@ -318,7 +318,10 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
  *   seq_lens     i32 [B]; outside [0, max_blocks * 16]: TQ_DEVERR_SEQLEN_RANGE, rows give 0.
  *   window, sinks  >= 0.
  * Code widths as in tq_paged_decode (each of 2, 3, 4, 8); D 64, 128 or 256; H_q a multiple of
- * H_kv, any ratio; block_size 16; H_kv <= 65535 (TQ_ERR_UNSUPPORTED otherwise).
+ * H_kv; block_size 16; H_kv <= 65535, max_q * H_q / H_kv <= 524280, and B * H_kv * tiles of 8
+ * query rows < 2^28 (TQ_ERR_UNSUPPORTED otherwise).
+ * The operands of the two contractions are fp16 (sums and softmax statistics fp32): the result
+ * is within about 1e-3 of the exact one in 2-norm whatever the type of out.
  * Only tokens a row sees reach its result: whatever the others' norms hold (a stored NaN norm
  * included).  No workspace, no state between calls: calls may overlap on the GPU, and be captured.
  * Errors: TQ_ERR_INVALID_ARG / TQ_ERR_UNSUPPORTED (nothing enqueued), TQ_ERR_CUDA. */

@@ -611,7 +611,7 @@ tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* 
     return TQ_ERR_UNSUPPORTED;
   max_q = (int32_t)std::min<int64_t>(max_q, q.shape[0]);
   const int64_t group = h_q / h_kv;
-  if ((max_q * group + 7) / 8 > 65535) return TQ_ERR_UNSUPPORTED;   // row tiles: a grid dimension
+  if ((max_q * group + 7) / 8 > 65535) return TQ_ERR_UNSUPPORTED;   // rows are counted in 32 bits
   if (B == 0 || q.shape[0] == 0) return TQ_OK;
   DeviceState* ds = nullptr;
   const tq_status s = device_state(&ds);
