@@ -323,7 +323,8 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
  * The operands of the two contractions are fp16 (sums and softmax statistics fp32): the result
  * is within about 1e-3 of the exact one in 2-norm whatever the type of out.
  * Only tokens a row sees reach its result: whatever the others' norms hold (a stored NaN norm
- * included).  No workspace, no state between calls: calls may overlap on the GPU, and be captured.
+ * included).  No workspace, no state between calls: calls may overlap on the GPU, and be captured (the
+ * library's first call on a device outside any capture).
  * Errors: TQ_ERR_INVALID_ARG / TQ_ERR_UNSUPPORTED (nothing enqueued), TQ_ERR_CUDA. */
 TQ_API tq_status tq_paged_attend(tq_tensor out, tq_tensor q, tq_tensor q_starts, tq_tensor pages,
                                  tq_tensor block_table, tq_tensor seq_lens,
@@ -361,7 +362,8 @@ TQ_API tq_status tq_paged_decode_window(tq_tensor out, tq_tensor q, tq_tensor pa
  * released by a call are free for the next one.  Table entries outside [0, num_blocks) raise
  * TQ_DEVERR_BLOCK_RANGE where a count would change, and are skipped.
  * Calls that share tables, counts or pages must be ordered on the GPU.  No workspace; nothing
- * is allocated; every call can be captured.
+ * is allocated; every call can be captured (the library's first call on a device outside any
+ * capture).
  * Limits (TQ_ERR_UNSUPPORTED): num_blocks <= 2^21, B and the number of pairs <= 8192,
  * max_blocks < 2^26.
  * Errors: TQ_ERR_INVALID_ARG / TQ_ERR_UNSUPPORTED (nothing enqueued), TQ_ERR_CUDA. */

@@ -163,12 +163,18 @@ def _dtype_code(t) -> int:
 _PACK = [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack for n in range(5)]
 
 
+_from_bytes = TensorDesc.from_buffer_copy
+
+
 def _desc(t) -> TensorDesc:
     shape = t.shape
     n = len(shape)
     if n > 4:
         raise ValueError("tensors of rank > 4 are not supported")
-    return TensorDesc.from_buffer_copy(_PACK[n](t.data_ptr(), _dtype_code(t), n, *shape, *t.stride()))
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        code = _dtype_code(t)
+    return _from_bytes(_PACK[n](t.data_ptr(), code, n, *shape, *t.stride()))
 
 
 def _stream_handle(stream, device):
@@ -396,9 +402,9 @@ def _descs(*tensors):
     index = tensors[0].get_device()
     out = []
     for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("all tensors must live on a CUDA device (no CPU fallback)")
-        if t.get_device() != index:
+        if t.get_device() != index or index < 0:
+            if not t.is_cuda:
+                raise ValueError("all tensors must live on a CUDA device (no CPU fallback)")
             raise ValueError(f"tensors on {tensors[0].device} and {t.device}: one device is needed")
         out.append(_desc(t))
     return out, index

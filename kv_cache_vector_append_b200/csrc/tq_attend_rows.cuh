@@ -29,7 +29,6 @@
 namespace tq {
 
 constexpr int kRowsWarps = 8;
-constexpr int kRowsMaxCtas = 8;            // CTAs of a cluster
 // most row tiles of 8 a CTA takes: as many accumulators as 128 registers a thread hold at
 // D = 64, twice that at D = 128
 __host__ __device__ constexpr int rows_tiles(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }

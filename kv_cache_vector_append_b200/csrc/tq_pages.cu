@@ -30,8 +30,10 @@ tq_status launch_plan(const PlanParams& p, const PageLayers& layers, const Devic
   const size_t smem = plan_smem(p.pool, ctas, p.requests, FORK ? p.batch : 0);
   if (smem + 1024 > (size_t)di.max_smem_optin) return TQ_ERR_UNSUPPORTED;
   auto kern = *fused ? pages_plan_kernel<FORK, true> : pages_plan_kernel<FORK, false>;
-  if (smem > 40 * 1024 &&                  // (48 KB with the static part need no opting in)
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  // (48 KB with the static part need no opting in; the same value always, as threads may call
+  // at once)
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               di.max_smem_optin - 1024) != cudaSuccess)
     return TQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
