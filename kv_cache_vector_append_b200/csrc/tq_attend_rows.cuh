@@ -11,15 +11,18 @@
 //
 // Layout.  A cluster of CTAs serves 8 NT rows of one (sequence, KV head); its warps take the
 // 16-token pages that some row sees in turn, each warp straight from global memory into
-// registers, one page ahead, and both contractions run on mma.sync m16n8k16 (M = tokens or
-// coordinates, N = 8 rows): the tile is 16 x 8 NT, far below what a tcgen05 tile needs, and
-// a page's lookups serve its NT row tiles.  Codes become fp16 through the pair tables of
-// tq_decode.cuh (one 256-byte row an entry, so the 32 lanes of a lookup hit 32 banks; 2-bit V
-// codes four at a time).  Pages that every row sees skip the masks.  The warps' partials
-// (M, l, O') are joined in shared memory, those of the cluster's CTAs over distributed shared
-// memory: no workspace, no counters, the same order of sums every time.
+// registers (each part of a page is reloaded for the next as soon as it has been used), and
+// both contractions run on mma.sync m16n8k16 (M = tokens or coordinates, N = 8 rows): the tile
+// is 16 x 8 NT, far below what a tcgen05 tile needs, and a page's lookups serve its NT row
+// tiles.  Codes become fp16 through the pair tables of tq_decode.cuh (one 256-byte row an
+// entry, so the 32 lanes of a lookup hit 32 banks; 2-bit V codes four at a time).  Pages that
+// every row sees skip the masks.  The warps' partials (M, l, O') are joined in shared memory,
+// those of the cluster's CTAs over distributed shared memory: no workspace, no counters, the
+// same order of sums every time.
 //
-// Bound: instruction issue next to the packed bytes, as the whole-sequence decode.
+// Bound: instruction issue (some 400 a page) and the L1 wavefronts of loads that touch eight
+// rows each.  64 windows of 4,096 tokens, 28/4 heads of 128, 4/2 bits: 49 us, 2.2 TB/s; a
+// block's start and end take about 8 us of it.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -29,8 +32,7 @@
 namespace tq {
 
 constexpr int kRowsWarps = 8;
-// most row tiles of 8 a CTA takes: as many accumulators as 128 registers a thread hold at
-// D = 64, twice that at D = 128
+// Most row tiles of 8 a CTA takes: 64 accumulators a thread (128 at D = 256, one tile's are 64).
 __host__ __device__ constexpr int rows_tiles(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
 
 // A thread's share of one row's packed codes, read from global memory with 4-byte loads.
@@ -186,34 +188,38 @@ attend_rows_kernel(const AttendParams p) {
     }
     return __shfl_sync(0xffffffffu, window, i % 32);
   };
-  struct Tile {
-    uint32_t kw0[KS::NW], kw1[KS::NW], vw[4][VS::NW];
-    float nK[2], nV[2];
+  // A page in registers, reloaded for the next page part by part as its parts have been used.
+  constexpr int KREG = C::KPACK + 4;                    // bytes of the K region
+  uint32_t kw0[KS::NW], kw1[KS::NW], vw[4][VS::NW];
+  float nK[2], nV[2];
+  const uint8_t* k_lane = p.pages + (int64_t)kvh * p.slot_stride + gid * p.row_stride;
+  const uint8_t* v_lane = p.pages + (int64_t)kvh * p.slot_stride + 2 * tig * p.row_stride + KREG;
+  auto load_keys = [&](int32_t id) {
+    const uint8_t* k = k_lane + (int64_t)id * p.blk_stride;
+    KS::load(kw0, k, tig);
+    KS::load(kw1, k + 8 * p.row_stride, tig);
   };
-  const uint8_t* lane_at = p.pages + (int64_t)kvh * p.slot_stride;
-  const int64_t k_at = gid * p.row_stride, v_at = 2 * tig * p.row_stride + p.k_region;
-  auto load_tile = [&](Tile& t, int32_t id) {
-    const uint8_t* base = lane_at + (int64_t)id * p.blk_stride;
-    const uint8_t* k0 = base + k_at;
-    const uint8_t* k1 = k0 + 8 * p.row_stride;
-    KS::load(t.kw0, k0, tig);
-    KS::load(t.kw1, k1, tig);
-    t.nK[0] = *(const float*)(k0 + C::KPACK);
-    t.nK[1] = *(const float*)(k1 + C::KPACK);
-    t.nV[0] = *(const float*)(k0 + p.k_region + C::VPACK);
-    t.nV[1] = *(const float*)(k1 + p.k_region + C::VPACK);
-    const uint8_t* v = base + v_at;
-    load_share<D, VB, 8>(t.vw[0], v, gid);
-    load_share<D, VB, 8>(t.vw[1], v + p.row_stride, gid);
+  auto load_rest = [&](int32_t id) {
+    const uint8_t* k = k_lane + (int64_t)id * p.blk_stride;
+    nK[0] = *(const float*)(k + C::KPACK);
+    nV[0] = *(const float*)(k + KREG + C::VPACK);
+    k += 8 * p.row_stride;
+    nK[1] = *(const float*)(k + C::KPACK);
+    nV[1] = *(const float*)(k + KREG + C::VPACK);
+    const uint8_t* v = v_lane + (int64_t)id * p.blk_stride;
+    load_share<D, VB, 8>(vw[0], v, gid);
+    load_share<D, VB, 8>(vw[1], v + p.row_stride, gid);
     v += 8 * p.row_stride;
-    load_share<D, VB, 8>(t.vw[2], v, gid);
-    load_share<D, VB, 8>(t.vw[3], v + p.row_stride, gid);
+    load_share<D, VB, 8>(vw[2], v, gid);
+    load_share<D, VB, 8>(vw[3], v + p.row_stride, gid);
   };
 
   // the first page is on its way while the tables and the queries are made
-  Tile next;
-  int32_t id = fetch(0);
-  if (id >= 0) load_tile(next, id);
+  int32_t cur = fetch(0);
+  if (cur >= 0) {
+    load_keys(cur);
+    load_rest(cur);
+  }
 
   rows_lut<KB, 0, false>(lut, p.kc, warp, lane);
   rows_lut<VB, 1, VQUAD>(lut, p.vc, kRowsWarps - 1 - warp, lane);
@@ -272,11 +278,15 @@ attend_rows_kernel(const AttendParams p) {
   auto look2 = [&](uint32_t a) { return *(const uint2*)(lut + a); };
 
   for (int i = 0; i < mine; ++i) {
-    const Tile t = next;
-    const int32_t cur = id;
-    id = i + 1 < mine ? fetch(i + 1) : -1;
-    if (id >= 0) load_tile(next, id);
-    if (cur < 0) continue;
+    const int32_t id = i + 1 < mine ? fetch(i + 1) : -1;
+    if (cur < 0) {
+      if (id >= 0) {
+        load_keys(id);
+        load_rest(id);
+      }
+      cur = id;
+      continue;
+    }
 
     // ---- S^T = K~ . Qhat^T ----
     float s[NT][4];
@@ -288,8 +298,8 @@ attend_rows_kernel(const AttendParams p) {
       constexpr int ks = decltype(KSI)::value;
       constexpr int b0 = KS::pos(4 * ks), b2 = KS::pos(4 * ks + 2);
       if constexpr (KB <= 4) {
-        const uint32_t a0 = look(lut_addr<b0, 2 * KB>(t.kw0, lk)), a1 = look(lut_addr<b0, 2 * KB>(t.kw1, lk));
-        const uint32_t a2 = look(lut_addr<b2, 2 * KB>(t.kw0, lk)), a3 = look(lut_addr<b2, 2 * KB>(t.kw1, lk));
+        const uint32_t a0 = look(lut_addr<b0, 2 * KB>(kw0, lk)), a1 = look(lut_addr<b0, 2 * KB>(kw1, lk));
+        const uint32_t a2 = look(lut_addr<b2, 2 * KB>(kw0, lk)), a3 = look(lut_addr<b2, 2 * KB>(kw1, lk));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
       } else {
@@ -300,10 +310,10 @@ attend_rows_kernel(const AttendParams p) {
           hi[i] = __byte_perm(ex, ey, 0x5410);
           lo[i] = __byte_perm(ex, ey, 0x7632);
         };
-        one(0, look(lut_addr<b0, KB>(t.kw0, lk)), look(lut_addr<b0 + KB, KB>(t.kw0, lk)));
-        one(1, look(lut_addr<b0, KB>(t.kw1, lk)), look(lut_addr<b0 + KB, KB>(t.kw1, lk)));
-        one(2, look(lut_addr<b2, KB>(t.kw0, lk)), look(lut_addr<b2 + KB, KB>(t.kw0, lk)));
-        one(3, look(lut_addr<b2, KB>(t.kw1, lk)), look(lut_addr<b2 + KB, KB>(t.kw1, lk)));
+        one(0, look(lut_addr<b0, KB>(kw0, lk)), look(lut_addr<b0 + KB, KB>(kw0, lk)));
+        one(1, look(lut_addr<b0, KB>(kw1, lk)), look(lut_addr<b0 + KB, KB>(kw1, lk)));
+        one(2, look(lut_addr<b2, KB>(kw0, lk)), look(lut_addr<b2 + KB, KB>(kw0, lk)));
+        one(3, look(lut_addr<b2, KB>(kw1, lk)), look(lut_addr<b2 + KB, KB>(kw1, lk)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_16816(s[nt], hi[0], hi[1], hi[2], hi[3], qb[nt][ks][0], qb[nt][ks][1]);
@@ -312,13 +322,15 @@ attend_rows_kernel(const AttendParams p) {
       }
     });
 
+    if (id >= 0) load_keys(id);
+
     // ---- online softmax: this thread's tokens gid + 8 r, rows 8 nt + 2 tig + e ----
     const int page0 = span.at(first + i * stride) * kBlockSize;
     // a page that every row sees whole needs no masks
     const bool full = page0 + kBlockSize - 1 <= pos_first &&
                       (page0 >= low_last || page0 + kBlockSize <= p.sinks);
     // floor at 2^-100 keeps 2^(s - M) finite for rows of (near) zero V norm
-    const float eV[2] = {fmaxf(log2_bound(t.nV[0]), -100.0f), fmaxf(log2_bound(t.nV[1]), -100.0f)};
+    const float eV[2] = {fmaxf(log2_bound(nV[0]), -100.0f), fmaxf(log2_bound(nV[1]), -100.0f)};
     float z[NT][2];
     bool need = false;
 #pragma unroll
@@ -326,7 +338,7 @@ attend_rows_kernel(const AttendParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) s[nt][2 * r + e] *= t.nK[r] * qscale[nt][e];
+        for (int r = 0; r < 2; ++r) s[nt][2 * r + e] *= nK[r] * qscale[nt][e];
         if (!full) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -368,7 +380,7 @@ attend_rows_kernel(const AttendParams p) {
           const float w = ex2_approx(s[nt][2 * r + e] - ref);       // 0 for a key the row does not see
           l[nt][e] += w;
           // whose norm may be anything
-          pv[e][r] = full || s[nt][2 * r + e] != -INFINITY ? w * t.nV[r] : 0.f;
+          pv[e][r] = full || s[nt][2 * r + e] != -INFINITY ? w * nV[r] : 0.f;
         }
       }
       pb[nt][0] = movmatrix_trans(pack_half2(pv[0][0], pv[1][0]));
@@ -387,10 +399,10 @@ attend_rows_kernel(const AttendParams p) {
       static_for<VS::NW>([&](auto JI) {
         constexpr int j = decltype(JI)::value;
         constexpr uint32_t M1 = 0x0F0F0F0Fu;
-        const uint32_t loAB = (t.vw[0][j] & M1) | ((t.vw[1][j] << 4) & ~M1);
-        const uint32_t hiAB = ((t.vw[0][j] >> 4) & M1) | (t.vw[1][j] & ~M1);
-        const uint32_t loCD = (t.vw[2][j] & M1) | ((t.vw[3][j] << 4) & ~M1);
-        const uint32_t hiCD = ((t.vw[2][j] >> 4) & M1) | (t.vw[3][j] & ~M1);
+        const uint32_t loAB = (vw[0][j] & M1) | ((vw[1][j] << 4) & ~M1);
+        const uint32_t hiAB = ((vw[0][j] >> 4) & M1) | (vw[1][j] & ~M1);
+        const uint32_t loCD = (vw[2][j] & M1) | ((vw[3][j] << 4) & ~M1);
+        const uint32_t hiCD = ((vw[2][j] >> 4) & M1) | (vw[3][j] & ~M1);
         static_for<8>([&](auto KI) {
           constexpr int k = decltype(KI)::value;
           const uint2 ab = look2(lut_addr1<8 * (k >> 1), 8>((k & 1) ? hiAB : loAB, lv));
@@ -403,10 +415,10 @@ attend_rows_kernel(const AttendParams p) {
       static_for<VS::NW>([&](auto JI) {
         constexpr int j = decltype(JI)::value;
         constexpr uint32_t M1 = 0x0F0F0F0Fu;
-        const uint32_t loAB = (t.vw[0][j] & M1) | ((t.vw[1][j] << 4) & ~M1);
-        const uint32_t hiAB = ((t.vw[0][j] >> 4) & M1) | (t.vw[1][j] & ~M1);
-        const uint32_t loCD = (t.vw[2][j] & M1) | ((t.vw[3][j] << 4) & ~M1);
-        const uint32_t hiCD = ((t.vw[2][j] >> 4) & M1) | (t.vw[3][j] & ~M1);
+        const uint32_t loAB = (vw[0][j] & M1) | ((vw[1][j] << 4) & ~M1);
+        const uint32_t hiAB = ((vw[0][j] >> 4) & M1) | (vw[1][j] & ~M1);
+        const uint32_t loCD = (vw[2][j] & M1) | ((vw[3][j] << 4) & ~M1);
+        const uint32_t hiCD = ((vw[2][j] >> 4) & M1) | (vw[3][j] & ~M1);
         static_for<4>([&](auto KI) {
           constexpr int k = decltype(KI)::value;
           add(std::integral_constant<int, j * 4 + k>{}, look(lut_addr1<8 * k, 8>(loAB, lv)),
@@ -427,10 +439,12 @@ attend_rows_kernel(const AttendParams p) {
         };
         using P0 = std::integral_constant<int, VS::pos(2 * mt)>;
         using P1 = std::integral_constant<int, VS::pos(2 * mt + 1)>;
-        add(MI, two(P0{}, t.vw[0], t.vw[1]), two(P1{}, t.vw[0], t.vw[1]), two(P0{}, t.vw[2], t.vw[3]),
-            two(P1{}, t.vw[2], t.vw[3]));
+        add(MI, two(P0{}, vw[0], vw[1]), two(P1{}, vw[0], vw[1]), two(P0{}, vw[2], vw[3]),
+            two(P1{}, vw[2], vw[3]));
       });
     }
+    if (id >= 0) load_rest(id);
+    cur = id;
   }
 
   // ---- the warps' partials [row][O' in natural order, M, l] ----
