@@ -6,7 +6,8 @@
 // statistics and accumulators are fp32.  fp16 operands: unit queries (2^-12 off, as their sum
 // over coordinates of either sign), centroids of keys times a factor in [1, 2) under which their
 // roundings are smallest (a search over 512 factors; it leaves with the rows' scales), values
-// c nV 2^-ev, P.  Together about 6e-4 of the output, a third of bf16's own rounding.  Key norms
+// c nV 2^-ev, P; 8-bit key centroids at D = 64 as hi + lo.  Together about 6e-4 of the output, a third of
+// bf16's own rounding.  Key norms
 // stay out of the operand: in it they would be rounded key by key, which costs 1e-3.
 // M >= max(x + log2 nV): a tile whose V norms lie within 2^8 of each other and which every row
 // sees takes the power 2^ev above its largest norm for all of them; in any other tile V~ = c,
@@ -50,8 +51,12 @@ template <int D, int KB, int VB>
 struct TilesCfg {
   static constexpr bool kTwoTiles = D <= 128;            // may hold two row tiles
   static constexpr bool kOneO = D == 256;                // one accumulator, one softmax warpgroup
+  // 8-bit key centroids as fp16 hi + lo, two parts of a K tile, at D = 64: there a tile has the room
+  // and the MMAs the time (195 against 205 us, 4 x 512 new tokens at 8,192, 14/2 heads; at D = 128
+  // 606 against 410 us), and the roundings of fewer coordinates weigh more.
+  static constexpr int KPARTS = KB == 8 && D == 64 ? 2 : 1, KPART = D / 64;   // (64-column blocks of a part)
   // bytes of a ring stage, keys of a tile
-  static constexpr int STAGE = D == 64 ? 16384 : 32768, N = STAGE / (2 * D), RING = 3;
+  static constexpr int STAGE = D == 64 ? 16384 * KPARTS : 32768, N = STAGE / (2 * D * KPARTS), RING = 3;
   static constexpr int PPT = N / kBlockSize;             // pages a tile
   // A slot works on items of NI keys of a tile, two score buffers in turn
   static constexpr int NI = N < 64 ? N : 64, H = N / NI;
@@ -64,7 +69,8 @@ struct TilesCfg {
   // norms [buffer][K, V][N]; a row tile whose key tiles alternate uses four buffers, at D <= 128
   // in the place of the second row tile's q
   static constexpr int NBUF = kOneO ? 4 : 2;
-  static constexpr int NORMS = NBUF * N * 2 * 4;
+  // (and at the start, behind the first buffer, 256 scales of q)
+  static constexpr int NORMS = 4 * (NBUF * N * 2 > N * 2 + 256 ? NBUF * N * 2 : N * 2 + 256);
   static constexpr int MISC = 1024;
   // more than half an SM: a CTA that holds all of tensor memory has the SM to itself
   static constexpr int RAW = OPER + LUT + NORMS + MISC;
@@ -585,6 +591,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
               const uint64_t ko = kd + (ks >> 2) * (N * 8) + (ks & 3) * 2;
               const uint32_t to = s_at + (n & 1) * 64;
               umma_bf16(to, qd, ko, f16_idesc(NI, false), ks > 0 ? 1u : 0u);
+              if constexpr (C::KPARTS == 2)
+                umma_bf16(to, qd, ko + C::KPART * (N * 8), f16_idesc(NI, false), 1u);
             }
             umma_commit(&ms->s_full[slot][n & 1]);
             if (half == C::H - 1) umma_commit(&ms->ring_empty[sl]);
@@ -655,8 +663,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     };
     auto look = [&](uint32_t a) { return *(const uint32_t*)(lut + a); };
     const uint32_t lk = 4u * lane, lv = 128u + 4u * lane;
-    // 16 codes to 16 halves
-    auto look_up = [&](auto IV, const auto& raw, int i, uint32_t (&h)[8]) {
+    // 16 codes to 16 halves (8 bits: and to what these leave)
+    auto look_up = [&](auto IV, const auto& raw, int i, uint32_t (&h)[8], uint32_t (&rest)[8]) {
       constexpr bool V = decltype(IV)::value;
       constexpr int BITS = V ? VB : KB, W = V ? C::VW : C::KW;
       const uint32_t off = V ? lv : lk;
@@ -668,8 +676,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
         if constexpr (BITS <= 4) {
           h[j] = look(lut_addr<2 * j * BITS, 2 * BITS>(r, off));
         } else {
-          h[j] = __byte_perm(look(lut_addr<2 * j * BITS, BITS>(r, off)),
-                             look(lut_addr<(2 * j + 1) * BITS, BITS>(r, off)), 0x5410);
+          const uint32_t a = look(lut_addr<2 * j * BITS, BITS>(r, off));
+          const uint32_t b = look(lut_addr<(2 * j + 1) * BITS, BITS>(r, off));
+          h[j] = __byte_perm(a, b, 0x5410);
+          rest[j] = __byte_perm(a, b, 0x7632);
         }
       });
     };
@@ -763,18 +773,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       constexpr bool V = decltype(IV)::value;
       uint8_t* stage = ring_s + (pos % C::RING) * C::STAGE;
       const uint8_t* at = nullptr;
-      constexpr int U = C::IT % 4 == 0 ? 4 : C::IT % 2 == 0 ? 2 : 1;   // rows in flight
+      constexpr bool REST = !V && C::KPARTS == 2;
+      constexpr int U = C::IT % 4 == 0 && !REST ? 4 : C::IT % 2 == 0 ? 2 : 1;   // rows in flight
 #pragma unroll
       for (int i = 0; i < C::IT; i += U) {
-        uint32_t h[U][8];
+        uint32_t h[U][8], rest[U][8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) look_up(IV, raw, i + u, h[u]);
+        for (int u = 0; u < U; ++u) look_up(IV, raw, i + u, h[u], rest[u]);
         if constexpr (V) {
 #pragma unroll
           for (int u = 0; u < U; ++u) scale_row(h[u], mul, i + u);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) store_row(h[u], i + u, stage);
+        if constexpr (REST) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) store_row(rest[u], i + u, stage + C::KPART * (N * 128));
+        }
         if (more) {
 #pragma unroll
           for (int u = 0; u < U; ++u) load_rows(INV, coming, i + u, next, at);
