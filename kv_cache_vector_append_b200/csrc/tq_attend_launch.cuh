@@ -13,8 +13,9 @@ namespace tq {
 // Rows a KV head up to which the rows kernel is used (8 sequences of 4096 tokens, 32/8 heads of
 // 128, 4 bits: 16 rows 31 us against the tiles' 69 us, 64 rows 100 against 69).
 constexpr int kRowsMost = 32;
+constexpr int kAttendMaxCtas = 8;          // the portable cluster size
 
-// Launches the kernel as clusters of 1, 2, 4 or 8 CTAs that split the keys of a group of rows.  Of the
+// Launches the kernel as clusters of 1 to 8 CTAs that split the keys of a group of rows.  Of the
 // counts that leave a CTA `least` units of keys or more, the one is taken whose waves of CTAs
 // times a CTA's time are least; alone and joined are the times of a CTA's start and end in
 // units of keys, without and with a join.
@@ -39,21 +40,25 @@ tq_status launch_attend(AttendParams p, int64_t tiles, int threads, int smem, in
     attr[0].val.clusterDim.x = (unsigned)ctas;
     cfg.gridDim = dim3((unsigned)(groups * ctas));
   };
-  // clusters of each size that the GPU holds at once (a property of the kernel)
-  static std::atomic<int> fit[4];
+  // clusters of each size that the GPU holds at once (a property of the kernel), -1 for none
+  static std::atomic<int> fit[kAttendMaxCtas];
   int best = 1;
   int64_t best_cost = 0;
-  for (int i = 0; i < 4; ++i) {
-    const int ctas = 1 << i;
-    if (i > 0 && units < (int64_t)ctas * least) break;
-    int n = fit[i].load(std::memory_order_relaxed);
+  for (int ctas = 1; ctas <= kAttendMaxCtas; ++ctas) {
+    if (ctas > 1 && units < (int64_t)ctas * least) break;
+    int n = fit[ctas - 1].load(std::memory_order_relaxed);
     if (n == 0) {
       grid(ctas);
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return TQ_ERR_CUDA;
-      fit[i].store(n, std::memory_order_relaxed);
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        if (ctas == 1) return TQ_ERR_CUDA;
+        cudaGetLastError();
+        n = -1;
+      }
+      fit[ctas - 1].store(n, std::memory_order_relaxed);
     }
-    const int64_t cost = (groups + n - 1) / n * ((i ? joined : alone) + (units + ctas - 1) / ctas);
-    if (i == 0 || cost < best_cost) {
+    if (n < 0) continue;
+    const int64_t cost = (groups + n - 1) / n * ((ctas > 1 ? joined : alone) + (units + ctas - 1) / ctas);
+    if (ctas == 1 || cost < best_cost) {
       best = ctas;
       best_cost = cost;
     }
