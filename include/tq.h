@@ -303,6 +303,7 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
  *   out[row, h] = sum_t softmax_t(scale * <q[row,h], k_hat_t>) v_hat_t, k_hat and v_hat as in
  *   tq_paged_decode.  A row that sees no token (p < 0, an empty sequence) gives 0.
  *   out, q       [rows, H_q, D] in bf16, f16 or f32 (out: f32 or q's dtype); last dim contiguous.
+ *                Rows of q may overlap (a broadcast dim), those of out may not.
  *   q_starts     i32 [B + 1] contiguous, ascending: rows [q_starts[b], q_starts[b+1]) of q and
  *                out belong to sequence b.  Rows outside [q_starts[0], q_starts[B]) are neither
  *                read nor written.

@@ -579,6 +579,13 @@ tq_status page_layers(const tq_tensor* layers, int32_t n, PageLayers* out, int64
 
 constexpr int64_t kMaxTableCols = (int64_t)1 << 26;
 
+// No two rows [i, j, :] of a three-dimensional array share an element.
+bool rows_apart(const tq_tensor& t) {
+  const int64_t n0 = t.shape[0], n1 = t.shape[1], d = t.shape[2], s0 = t.stride[0], s1 = t.stride[1];
+  if ((n0 > 1 && s0 < d) || (n1 > 1 && s1 < d)) return false;
+  return n0 < 2 || n1 < 2 || s0 >= s1 * (n1 - 1) + d || s1 >= s0 * (n0 - 1) + d;
+}
+
 // Validation and parameters of the attention over chunks and windows (q_starts null: one
 // row a sequence).
 tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* q_starts,
@@ -592,6 +599,7 @@ tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* 
     return TQ_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i)
     if (out.shape[i] != q.shape[i]) return TQ_ERR_INVALID_ARG;
+  if (!rows_apart(out)) return TQ_ERR_INVALID_ARG;
   if (!valid_array(pages, 4) || pages.dtype != TQ_U8 || pages.stride[3] != 1)
     return TQ_ERR_INVALID_ARG;
   const int64_t B = block_table.shape[0];

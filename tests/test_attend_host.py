@@ -42,6 +42,9 @@ def test_attend_refusals():
     assert _attend(out=_fake([9, 8, 128], B.BF16)) == bad
     assert _attend(q=_fake([10, 8, 128], B.I32), out=_fake([10, 8, 128], B.I32)) == bad
     assert _attend(q=_fake([10, 8, 128], B.BF16, strides=[2048, 256, 2])) == bad
+    assert _attend(out=_fake([10, 8, 128], B.BF16, strides=[0, 128, 1])) == bad      # rows of out overlap
+    assert _attend(out=_fake([10, 8, 128], B.BF16, strides=[1024, 0, 1])) == bad
+    assert _attend(out=_fake([10, 8, 128], B.BF16, strides=[512, 128, 1])) == bad
     assert _attend(starts=_fake([2], B.I32)) == bad                       # B + 1 entries
     assert _attend(starts=_fake([3], B.I64)) == bad
     assert _attend(lens=_fake([3], B.I32)) == bad

@@ -246,6 +246,20 @@ def test_rows_at_odd_addresses(q_lens, dtype):
         assert torch.equal(out.to(c.q.dtype), want)
 
 
+@pytest.mark.parametrize("q_lens", [[1, 2], [90, 40]])
+def test_broadcast_queries(q_lens):
+    """One query row for all heads (a dim of stride 0), and out head by head apart."""
+    tq = _tq()
+    c = Case(tq, 128, 8, 2, 4, 4, [300, 100], q_lens)
+    n = c.q.shape[0]
+    c.q = c.q[:, :1].expand(n, 8, 128)
+    want = c.run().clone()
+    check_rows(to_np_f64(want), *c.ref())
+    out = torch.zeros(8, n, 128, dtype=c.q.dtype, device="cuda").transpose(0, 1)
+    tq.paged_attend(out, c.q, c.starts, c.pages, c.table, c.lens, c.cb, SEED, c.scale, c.max_q)
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 40])
 def test_a_bad_entry_skips_its_page(rows):
     tq = _tq()
