@@ -321,7 +321,8 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
  * Code widths as in tq_paged_decode (each of 2, 3, 4, 8); D 64, 128 or 256; H_q a multiple of
  * H_kv; block_size 16; H_kv <= 65535, max_q * H_q / H_kv <= 524280, and B * H_kv * tiles of 8
  * query rows < 2^28 (TQ_ERR_UNSUPPORTED otherwise).
- * The operands of the two contractions are fp16 (sums and softmax statistics fp32): the result
+ * The operands of the two contractions are fp16, 8-bit key centroids twice that (hi + lo); sums
+ * and softmax statistics are fp32: the result
  * is within about 1e-3 of the exact one in 2-norm (2e-3 where a few keys have very large
  * norms), whatever the type of out.
  * Only tokens a row sees reach its result: whatever the others' norms hold (a stored NaN norm

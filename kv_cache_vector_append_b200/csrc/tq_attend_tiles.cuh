@@ -6,9 +6,9 @@
 // statistics and accumulators are fp32.  fp16 operands: unit queries (2^-12 off, as their sum
 // over coordinates of either sign), centroids of keys times a factor in [1, 2) under which their
 // roundings are smallest (a search over 512 factors; it leaves with the rows' scales), values
-// c nV 2^-ev, P; 8-bit key centroids at D = 64 as hi + lo.  Together about 6e-4 of the output, a third of
-// bf16's own rounding.  Key norms
-// stay out of the operand: in it they would be rounded key by key, which costs 1e-3.
+// c nV 2^-ev, P; 8-bit key centroids as hi + lo.  Together about 6e-4 of the output, a third of
+// bf16's own rounding.  Key norms stay out of the operand: in it they would be rounded key by
+// key, which costs 1e-3.
 // M >= max(x + log2 nV): a tile whose V norms lie within 2^8 of each other and which every row
 // sees takes the power 2^ev above its largest norm for all of them; in any other tile V~ = c,
 // P = 2^(x - M) nV, and the bound goes key by key, masks included, so that what a row does not
@@ -51,10 +51,12 @@ template <int D, int KB, int VB>
 struct TilesCfg {
   static constexpr bool kTwoTiles = D <= 128;            // may hold two row tiles
   static constexpr bool kOneO = D == 256;                // one accumulator, one softmax warpgroup
-  // 8-bit key centroids as fp16 hi + lo, two parts of a K tile, at D = 64: there a tile has the room
-  // and the MMAs the time (195 against 205 us, 4 x 512 new tokens at 8,192, 14/2 heads; at D = 128
-  // 606 against 410 us), and the roundings of fewer coordinates weigh more.
-  static constexpr int KPARTS = KB == 8 && D == 64 ? 2 : 1, KPART = D / 64;   // (64-column blocks of a part)
+  // 8-bit key centroids as fp16 hi + lo, two parts of a K tile: their cells are narrower than what
+  // keys of one direction differ by, so that roundings do not cancel in the softmax as those of
+  // coarser codes do (keys with channel means of 30 sigma: 6e-3 of the output without lo).  The
+  // tiles are half as long then (4 x 512 new tokens at 8,192, 8/8 bits: 32/8 heads of 128 723
+  // against 511 us, 16/4 heads of 256 1,128 against 856).
+  static constexpr int KPARTS = KB == 8 ? 2 : 1, KPART = D / 64;   // (64-column blocks of a part)
   // bytes of a ring stage, keys of a tile
   static constexpr int STAGE = D == 64 ? 16384 * KPARTS : 32768, N = STAGE / (2 * D * KPARTS), RING = 3;
   static constexpr int PPT = N / kBlockSize;             // pages a tile
@@ -414,8 +416,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     if (tid == 0) report_error(p.err, TQ_DEVERR_LAYOUT);
     return;
   }
-  // One thread issues the MMAs of a slot, in the order P V (n - 2), Q K (n); a shared O' has one
-  // thread for all.
+  // One thread issues the MMAs of a slot, in the order P V (n - ahead), Q K (n); a shared O' has
+  // one thread for all.
   constexpr int kIssuers = C::kOneO ? 1 : 2;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -561,9 +563,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       const uint64_t q = sw128_desc(smem_u32(q_s) + (two ? slot * C::QTILE : 0));
       const uint32_t ring_at = smem_u32(ring_s);
       bool ok = C::kOneO || tile_wait(&ms->q_ready, 0, p.wait_ms);
-      for (int n = 0; n < items + 2 && __all_sync(0xffffffffu, ok); ++n) {
-        if (n >= 2) {                                    // P V of item n - 2
-          const int m = n - 2, at = v_at(slot_tile(slot, m / C::H)), sl = at % C::RING, half = m % C::H;
+      // Q K runs ahead of P V by two items.  A slot that takes every other tile, of one item each,
+      // runs one ahead: then it has seen V of its last tile full, and with it every earlier ring
+      // position, before it waits for K's, so that no wait skips a phase of its barrier.
+      const int ahead = two || C::kOneO || C::H > 1 ? 2 : 1;
+      for (int n = 0; n < items + ahead && __all_sync(0xffffffffu, ok); ++n) {
+        if (n >= ahead) {                                // P V of item n - ahead
+          const int m = n - ahead, at = v_at(slot_tile(slot, m / C::H)), sl = at % C::RING, half = m % C::H;
           ok = (half || tile_wait(&ms->ring_full[sl], (uint32_t)(at / C::RING) & 1u, p.wait_ms)) &&
                tile_wait(&ms->p_ready[slot][m & 1], (uint32_t)(m >> 1) & 1u, p.wait_ms);
           if (!__all_sync(0xffffffffu, ok)) break;
