@@ -117,4 +117,31 @@ __device__ __forceinline__ AttendSpan attend_span(const AttendParams& p, int p0,
   return s;
 }
 
+// The factor 1 + j / 512 in [1, 2) under which the centroids of a table lie nearest to fp16 numbers
+// (it leaves with the queries' scales).  The first: a warp's best of the factors of its threads, the
+// least squared rounding (14 bits of it) with j below; the least of all warps' is the call's.
+template <int BITS>
+__device__ __forceinline__ unsigned centroid_factor_key(const float* c, int t, int threads) {
+  float2 pair[1 << (BITS - 1)];
+#pragma unroll
+  for (int i = 0; i < 1 << (BITS - 1); ++i) pair[i] = make_float2(__ldg(c + 2 * i), __ldg(c + 2 * i + 1));
+  unsigned key = ~0u;
+  for (int j = t; j < 512; j += threads) {
+    const float a = 1.0f + (float)j * (1.0f / 512);
+    float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 1 << (BITS - 1); ++i) {
+      const float x = pair[i].x * a, y = pair[i].y * a;
+      const float2 r = __half22float2(__floats2half2_rn(x, y));
+      e0 = fmaf(r.x - x, r.x - x, e0);
+      e1 = fmaf(r.y - y, r.y - y, e1);
+    }
+    key = min(key, (__float_as_uint((e0 + e1) / (a * a)) & ~511u) | (unsigned)j);
+  }
+  return __reduce_min_sync(0xffffffffu, key);
+}
+__device__ __forceinline__ float centroid_factor(unsigned key) {
+  return 1.0f + (float)(key & 511u) * (1.0f / 512);
+}
+
 }  // namespace tq

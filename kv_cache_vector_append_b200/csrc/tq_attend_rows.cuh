@@ -5,9 +5,9 @@
 //   s_t = scale log2(e) nK_t <q', cK[i_t]>,   o = R^T (sum_t 2^(s_t - M) nV_t cV[j_t]) / l,
 // l = sum_t 2^(s_t - M): the queries are rotated once and the output once, keys and values
 // are never rebuilt.  Sums, maxima and l are fp32; the operands of the two contractions are
-// fp16: unit queries and centroids (2^-12 off; 8-bit key centroids as hi + lo), and weights
-// P = 2^(s - M) nV <= 2^9 with M >= max(s + log2 nV), so that the weights keep fp16's range
-// whatever the norms are.
+// fp16: unit queries and centroids (2^-12 off; key centroids times a factor in [1, 2) under which
+// their roundings are smallest, 8-bit ones as hi + lo), and weights P = 2^(s - M) nV <= 2^9 with
+// M >= max(s + log2 nV), so that the weights keep fp16's range whatever the norms are.
 //
 // Layout.  A cluster of CTAs serves 8 NT rows of one (sequence, KV head); its warps take the
 // 16-token pages that some row sees in turn, each warp straight from global memory into
@@ -86,7 +86,7 @@ struct KeyShare {
 // entry's half row with 16-byte stores.  VQUAD: 2-bit V codes four at a time, as
 // lut_build_vquad lays them out.
 template <int BITS, int HALF, bool VQUAD>
-__device__ __forceinline__ void rows_lut(uint8_t* lut, const float* c, int warp, int lane) {
+__device__ __forceinline__ void rows_lut(uint8_t* lut, const float* c, float factor, int warp, int lane) {
   constexpr int kEntries = VQUAD ? 256 : lut_entries(BITS);
   for (int e0 = warp * 32; e0 < kEntries; e0 += kRowsWarps * 32) {
     const int e = e0 + lane;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void rows_lut(uint8_t* lut, const float* c, int warp,
         v = pack_half2(c[e & 3], c[(e >> 4) & 3]);
         v2 = pack_half2(c[(e >> 2) & 3], c[e >> 6]);
       } else if constexpr (BITS <= 4) {
-        v = pack_half2(c[e & ((1 << BITS) - 1)], c[e >> BITS]);
+        v = pack_half2(c[e & ((1 << BITS) - 1)] * factor, c[e >> BITS] * factor);
       } else {
         const float hi = __half2float(__float2half_rn(c[e]));
         v = pack_half2(hi, c[e] - hi);
@@ -148,6 +148,12 @@ attend_rows_kernel(const AttendParams p) {
   const int b = item.b, kvh = item.kvh, G = p.group;
 
   const AttendSeq sq = attend_seq(p, b, tid == 0 && split == 0 && kvh == 0 && item.tile == 0);
+  // while the sequence's numbers are on their way
+  __shared__ unsigned factor_key[kRowsWarps];
+  if constexpr (KB <= 4) {
+    const unsigned key = centroid_factor_key<KB>(p.kc, tid, kRowsWarps * 32);
+    if (lane == 0) factor_key[warp] = key;
+  }
   // this cluster's rows [r0, r0 + rows) of the KV head's n_q * G
   const int r0 = item.tile * ROWS;
   const int rows = min(ROWS, sq.n_q * G - r0);
@@ -221,8 +227,7 @@ attend_rows_kernel(const AttendParams p) {
     load_rest(cur);
   }
 
-  rows_lut<KB, 0, false>(lut, p.kc, warp, lane);
-  rows_lut<VB, 1, VQUAD>(lut, p.vc, kRowsWarps - 1 - warp, lane);
+  rows_lut<VB, 1, VQUAD>(lut, p.vc, 1.0f, kRowsWarps - 1 - warp, lane);
   // q' of a row by a warp: sign flips, FWHT, 1/sqrt(D), then to unit length in fp16
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
@@ -247,6 +252,14 @@ attend_rows_kernel(const AttendParams p) {
     if (lane == 0) qsc[r] = nrm * p.scale_log2;
   }
   __syncthreads();
+  float factor = 1.0f;                        // of the key centroids
+  if constexpr (KB <= 4) {
+    unsigned key = factor_key[0];
+#pragma unroll
+    for (int i = 1; i < kRowsWarps; ++i) key = min(key, factor_key[i]);
+    factor = centroid_factor(key);
+  }
+  rows_lut<KB, 0, false>(lut, p.kc, factor, warp, lane);
 
   uint32_t qb[NT][C::KSTEPS][2];
   // this thread's rows 8 nt + 2 tig + e: scale, position, first key of the window
@@ -262,7 +275,7 @@ attend_rows_kernel(const AttendParams p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * nt + 2 * tig + e;
-      qscale[nt][e] = qsc[r];
+      qscale[nt][e] = qsc[r] / factor;
       pos[nt][e] = r < rows ? p0 + (r0 + r) / G : -1;
       low[nt][e] = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos[nt][e] - p.window + 1) : 0;
       M[nt][e] = -INFINITY;
@@ -273,6 +286,7 @@ attend_rows_kernel(const AttendParams p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[nt][mt][k] = 0.f;
   }
+  __syncthreads();                            // the tables are there
   const uint32_t lk = 4u * lane, lv = 128u + (VQUAD ? 8u * (lane & 15) : 4u * lane);
   auto look = [&](uint32_t a) { return *(const uint32_t*)(lut + a); };
   auto look2 = [&](uint32_t a) { return *(const uint2*)(lut + a); };

@@ -101,7 +101,7 @@ struct TileInfo {
 struct TilesMisc {
   uint4 flip[32];                          // sign bits of the coordinates, as in a 16-bit row
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2], norm_full[4], ring_full[3], ring_empty[3], o_done, q_ready;
-  unsigned long long best;
+  unsigned best;                           // the key centroids' factor (centroid_factor_key)
   float alpha;
   uint32_t tmem;
   int tok[4][8];                           // first token of a page of the tile; < 0: no page
@@ -226,33 +226,6 @@ __device__ __forceinline__ void tiles_lut(uint8_t* lut, const float* c, float al
       if (j < kEntries) row[j * (kLutRow / 4)] = __shfl_sync(0xffffffffu, v, j);
   }
 }
-// The factor whose scaled centroids lie nearest to fp16 numbers: 1 + best / 512.
-template <int BITS>
-__device__ __forceinline__ void tiles_alpha(const float* c, int t, int threads, unsigned long long* best) {
-  if constexpr (BITS <= 4) {
-    unsigned long long key = ~0ull;
-    for (int j = t; j < 512; j += threads) {
-      const float a = 1.0f + (float)j * (1.0f / 512);
-      float err = 0.f;
-      for (int i = 0; i < 1 << BITS; ++i) {
-        const float x = c[i] * a, d = __half2float(__float2half_rn(x)) - x;
-        err = fmaf(d, d, err);
-      }
-      const unsigned long long k = ((unsigned long long)__float_as_uint(err / (a * a)) << 32) | (unsigned)j;
-      key = k < key ? k : key;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
-      key = other < key ? other : key;
-    }
-    if ((t & 31) == 0) atomicMin(best, key);
-  }
-}
-__device__ __forceinline__ float tiles_factor(unsigned long long best) {
-  return 1.0f + (float)(unsigned)best * (1.0f / 512);
-}
-
 // A row of D coordinates over D / 16 lanes: lane l of the group holds, in x[4 j + e], coordinate
 // 4 (l + D / 16 j) + e, so that a group's accesses of 4 coordinates a lane are contiguous.
 template <int D>
@@ -434,7 +407,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
     }
     mbar_init(&ms->o_done, kIssuers);
     mbar_init(&ms->q_ready, 8);                          // the softmax warps
-    ms->best = ~0ull;
+    ms->best = ~0u;
     fence_mbar_init();
   }
   if (warp == 12) tmem_alloc(&ms->tmem, 512);
@@ -522,12 +495,18 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       }
     }
   };
+  auto find_factor = [&](int t, int threads) {
+    if constexpr (KB <= 4) {
+      const unsigned key = centroid_factor_key<KB>(p.kc, t, threads);
+      if (lane == 0) atomicMin(&ms->best, key);
+    }
+  };
   if constexpr (C::kOneO) {
     // D = 256: a thread cannot hold a row; every warp takes rows, then the tables
-    tiles_alpha<KB>(p.kc, tid, kTilesThreads, &ms->best);
+    find_factor(tid, kTilesThreads);
     make_q(warp, kTilesWarps);
     __syncthreads();                                     // the best factors are known
-    if (KB <= 4) ak = tiles_factor(ms->best);
+    if (KB <= 4) ak = centroid_factor(ms->best);
     tiles_lut<KB, 0>(lut, p.kc, ak, warp, kTilesWarps, lane);
     tiles_lut<VB, 1>(lut, p.vc, 1.0f, kTilesWarps - 1 - warp, kTilesWarps, lane);
     if (warp < 8) qs = qs_s[srow] / ak;
@@ -821,9 +800,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
       if constexpr (C::kDeep) load_all(VI{}, raw_v, b0);
       if constexpr (!C::kOneO) {                         // the tables, while these come in
         tiles_lut<VB, 1>(lut, p.vc, 1.0f, w, kDequantWarps, lane);
-        tiles_alpha<KB>(p.kc, tid - 256, 128, &ms->best);
+        find_factor(tid - 256, 128);
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (KB <= 4) ak = tiles_factor(ms->best);
+        if (KB <= 4) ak = centroid_factor(ms->best);
         if (tid == 256) ms->alpha = ak;                  // read past norm_full
         tiles_lut<KB, 0>(lut, p.kc, ak, w, kDequantWarps, lane);
         asm volatile("bar.sync 1, 128;" ::: "memory");

@@ -94,3 +94,11 @@ def _check_mean_keys(d, hq, hkv, kb, vb, lens, q_lens, mean):
                                               (256, 8, [1500], [40])])
 def test_8_bit_keys_that_share_a_direction_in_chunks(d, vb, lens, q_lens, mean):
     _check_mean_keys(d, 4, 2, 8, vb, lens, q_lens, mean)
+
+
+@pytest.mark.parametrize("mean", [0, 10, 30])
+@pytest.mark.parametrize("d,kb,vb,q_len", [(256, 3, 4, 12), (256, 4, 2, 16), (128, 4, 4, 4), (128, 3, 8, 14),
+                                           (64, 4, 3, 16), (64, 2, 4, 8), (128, 8, 4, 16), (256, 8, 8, 16),
+                                           (256, 3, 4, 40), (128, 4, 4, 40), (64, 4, 3, 80)])
+def test_keys_that_share_a_direction(d, kb, vb, q_len, mean):
+    _check_mean_keys(d, 4, 2, kb, vb, [300, 417, 333, 512, 100], [q_len] * 5, mean)
