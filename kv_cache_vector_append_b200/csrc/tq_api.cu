@@ -638,7 +638,7 @@ tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* 
   p.batch = (int32_t)B;
   p.q_starts = q_starts != nullptr ? (const int32_t*)q_starts->data : nullptr;
   p.num_rows = (int32_t)q.shape[0];
-  p.max_q = std::max(max_q, 1);
+  p.max_q = max_q;
   p.q = q.data;
   p.q_rstride = q.stride[0];
   p.q_hstride = q.stride[1];

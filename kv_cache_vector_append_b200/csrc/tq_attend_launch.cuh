@@ -24,6 +24,7 @@ tq_status launch_attend(AttendParams p, int64_t tiles, int threads, int smem, in
                         int alone, int joined, int least, cudaStream_t st) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
+  tiles = std::max<int64_t>(tiles, 1);       // max_q = 0: ranges are still checked
   const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
   if (groups > 0x7fffffff / 8) return TQ_ERR_UNSUPPORTED;
   p.row_tiles = (int32_t)tiles;
