@@ -319,7 +319,7 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
  *   seq_lens     i32 [B]; outside [0, max_blocks * 16]: TQ_DEVERR_SEQLEN_RANGE, rows give 0.
  *   window, sinks  >= 0.
  * Code widths as in tq_paged_decode (each of 2, 3, 4, 8); D 64, 128 or 256; H_q a multiple of
- * H_kv; block_size 16; H_kv <= 65535, max_q * H_q / H_kv <= 524280, and B * H_kv * tiles of 8
+ * H_kv; block_size 16; H_kv <= 65535, max_q * H_q / H_kv < 2^22, and B * H_kv * tiles of 8
  * query rows < 2^28 (TQ_ERR_UNSUPPORTED otherwise).
  * The operands of the two contractions are fp16, 8-bit key centroids twice that (hi + lo); sums
  * and softmax statistics are fp32: the result

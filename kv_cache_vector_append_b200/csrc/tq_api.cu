@@ -578,6 +578,8 @@ tq_status page_layers(const tq_tensor* layers, int32_t n, PageLayers* out, int64
 }
 
 constexpr int64_t kMaxTableCols = (int64_t)1 << 26;
+// Query rows of a KV head in one sequence (the kernels count rows and row tiles in 32 bits).
+constexpr int64_t kMaxHeadRows = (int64_t)1 << 22;
 
 // No two rows [i, j, :] of a three-dimensional array share an element.
 bool rows_apart(const tq_tensor& t) {
@@ -619,7 +621,7 @@ tq_status attend_run(const tq_tensor& out, const tq_tensor& q, const tq_tensor* 
     return TQ_ERR_UNSUPPORTED;
   max_q = (int32_t)std::min<int64_t>(max_q, q.shape[0]);
   const int64_t group = h_q / h_kv;
-  if ((max_q * group + 7) / 8 > 65535) return TQ_ERR_UNSUPPORTED;   // rows are counted in 32 bits
+  if (max_q * group >= kMaxHeadRows) return TQ_ERR_UNSUPPORTED;
   if (B == 0 || q.shape[0] == 0) return TQ_OK;
   DeviceState* ds = nullptr;
   const tq_status s = device_state(&ds);
