@@ -38,8 +38,6 @@ __global__ void dyn_smem_base_probe() {
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 struct DeviceState {
   // device address of g_tq_error_word; published (release) last by the one-time set-up,
   // so a non-null value means `info` is complete

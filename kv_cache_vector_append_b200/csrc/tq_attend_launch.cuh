@@ -2,11 +2,11 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 
 #include "tq_attend_rows.cuh"
 #include "tq_attend_tiles.cuh"
 #include "tq_launch.cuh"
+#include "tq_memo.cuh"
 
 namespace tq {
 
@@ -22,8 +22,10 @@ constexpr int kAttendMaxCtas = 8;          // the portable cluster size
 template <auto kern>
 tq_status launch_attend(AttendParams p, int64_t tiles, int threads, int smem, int64_t units,
                         int alone, int joined, int least, cudaStream_t st) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return TQ_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices ||
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return cuda_failed();
   tiles = std::max<int64_t>(tiles, 1);       // max_q = 0: ranges are still checked
   const int64_t groups = (int64_t)p.batch * p.h_kv * tiles;
   if (groups > 0x7fffffff / 8) return TQ_ERR_UNSUPPORTED;
@@ -41,23 +43,22 @@ tq_status launch_attend(AttendParams p, int64_t tiles, int threads, int smem, in
     attr[0].val.clusterDim.x = (unsigned)ctas;
     cfg.gridDim = dim3((unsigned)(groups * ctas));
   };
-  // clusters of each size that the GPU holds at once (a property of the kernel), -1 for none
-  static std::atomic<int> fit[kAttendMaxCtas];
+  // clusters of each size that the device holds at once (0: none of that size)
+  static Memo<kMaxDevices * kAttendMaxCtas> fit;
   int best = 1;
   int64_t best_cost = 0;
   for (int ctas = 1; ctas <= kAttendMaxCtas; ++ctas) {
     if (ctas > 1 && units < (int64_t)ctas * least) break;
-    int n = fit[ctas - 1].load(std::memory_order_relaxed);
-    if (n == 0) {
+    int n = 0;
+    const bool known = fit.get(dev * kAttendMaxCtas + ctas - 1, [&](int* a) {
       grid(ctas);
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-        if (ctas == 1) return TQ_ERR_CUDA;
-        cudaGetLastError();
-        n = -1;
-      }
-      fit[ctas - 1].store(n, std::memory_order_relaxed);
+      return cudaOccupancyMaxActiveClusters(a, kern, &cfg) == cudaSuccess;
+    }, &n);
+    if (!known || n < 1) {
+      if (ctas == 1) return cuda_failed();
+      if (!known) cuda_failed();
+      continue;
     }
-    if (n < 0) continue;
     const int64_t cost = (groups + n - 1) / n * ((ctas > 1 ? joined : alone) + (units + ctas - 1) / ctas);
     if (ctas == 1 || cost < best_cost) {
       best = ctas;
@@ -65,7 +66,7 @@ tq_status launch_attend(AttendParams p, int64_t tiles, int threads, int smem, in
     }
   }
   grid(best);
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return TQ_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return cuda_failed();
   return launch_status();
 }
 
@@ -89,11 +90,16 @@ template <int D, int KB, int VB>
 tq_status launch_tiles_t(AttendParams p, cudaStream_t st) {
   using C = TilesCfg<D, KB, VB>;
   // the split of registers between the warpgroups counts on the launch's own number
-  static const bool regs_ok = [] {
-    cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, attend_tiles_kernel<D, KB, VB>) == cudaSuccess && a.numRegs == kTilesRegs;
-  }();
-  if (!regs_ok) return TQ_ERR_CUDA;
+  static Memo<1> regs;
+  int n = 0;
+  if (!regs.get(0, [](int* a) {
+        cudaFuncAttributes f{};
+        if (cudaFuncGetAttributes(&f, attend_tiles_kernel<D, KB, VB>) != cudaSuccess) return false;
+        *a = f.numRegs;
+        return true;
+      }, &n))
+    return cuda_failed();
+  if (n != kTilesRegs) return TQ_ERR_CUDA;
   const int64_t rows = (int64_t)p.max_q * p.group;
   p.tile_rows = C::kTwoTiles && rows > kTileRows ? 2 * kTileRows : kTileRows;
   const int64_t units = (attend_pages(p, p.tile_rows / p.group) + C::PPT - 1) / C::PPT;

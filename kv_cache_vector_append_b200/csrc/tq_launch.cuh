@@ -13,6 +13,8 @@
 
 namespace tq {
 
+constexpr int kMaxDevices = 64;
+
 struct DeviceInfo {
   int num_sms = 0;
   int max_smem_optin = 0;
@@ -39,6 +41,12 @@ struct DecodePlan {
 
 inline tq_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+// A call of the runtime failed: its error must not be read as that of a later launch.
+inline tq_status cuda_failed() {
+  cudaGetLastError();
+  return TQ_ERR_CUDA;
 }
 
 tq_status launch_append_any(int dim, int dtype, const AppendParams& p, const AppendMaps& maps,

@@ -34,7 +34,7 @@ tq_status launch_plan(const PlanParams& p, const PageLayers& layers, const Devic
   // at once)
   if (smem > 40 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                di.max_smem_optin - 1024) != cudaSuccess)
-    return TQ_ERR_CUDA;
+    return cuda_failed();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPlanThreads);
@@ -46,7 +46,7 @@ tq_status launch_plan(const PlanParams& p, const PageLayers& layers, const Devic
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p, few, pieces) != cudaSuccess) return TQ_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, p, few, pieces) != cudaSuccess) return cuda_failed();
   return launch_status();
 }
 
