@@ -66,7 +66,7 @@ tq_status launch_pages_fork(const PlanParams& p, const PageLayers& layers, const
   bool fused = false;
   const tq_status s = launch_plan<true>(p, layers, di, st, &fused);
   if (s != TQ_OK || fused) return s;
-  const int chunks = (p.cols + kForkChunk - 1) / kForkChunk;
+  const int chunks = std::min((p.cols + kForkChunk - 1) / kForkChunk, kForkMostChunks);
   pages_fork_kernel<<<dim3(p.requests, chunks + layers.count), kPagesThreads, 0, st>>>(p, layers,
                                                                                        chunks);
   return launch_status();

@@ -408,7 +408,8 @@ pages_resize_kernel(const PlanParams p, const __grid_constant__ PageLayers layer
   }
 }
 
-constexpr int kForkChunk = 4 * kPagesThreads;   // table entries a CTA shares
+constexpr int kForkChunk = 4 * kPagesThreads;   // table entries a CTA shares at a time
+constexpr int kForkMostChunks = 32768;          // (chunks + layers is a grid's second dimension)
 
 // Second launch of fork: grid (pairs, chunks of the table row + layers).  The entries of the
 // parent's full pages are shared with the child, its partly filled one is copied.
@@ -425,7 +426,8 @@ pages_fork_kernel(const PlanParams p, const __grid_constant__ PageLayers layers,
   const int len = p.seq_lens[child];       // the parent's before the call
   // a partly filled last page without a copy is a hole (or out of range) in the parent too
   const int end = from >= 0 ? len / kPageTokens : pages_of(len);
-  share_entries(p, p.parents[i], child, end, blockIdx.y * kForkChunk, kPagesThreads, threadIdx.x);
+  for (int c0 = blockIdx.y * kForkChunk; c0 < end; c0 += chunks * kForkChunk)
+    share_entries(p, p.parents[i], child, end, c0, kPagesThreads, threadIdx.x);
 }
 
 struct CompactParams {

@@ -120,3 +120,29 @@ def test_random_runs_in_two_launches(layers):
             p.fork(tq, [rng.randrange(batch) for _ in children], children)
     assert tq.get_device_error() in (0, tq.DEVERR_NO_PAGES)
     assert pages_of(int(p.lens.max())) > 1024
+
+
+def test_the_widest_table():
+    """2^26 - 1 columns: a fork's grid ends below what a launch takes, and it loops."""
+    tq = _tq()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")     # noqa: E731
+    cols, pool = (1 << 26) - 1, 40_000
+    table = torch.full((2, cols), -1, dtype=torch.int32, device="cuda")
+    pages = torch.zeros(pool, BS, 1, 8, dtype=torch.uint8, device="cuda")
+    lens, refs, moves = i32([0, 0]), torch.zeros(pool, dtype=torch.int32, device="cuda"), i32([[9, 9]] * 2)
+    n = 33_000 * BS + 5                                     # 33,001 pages
+    tq.pages_resize(pages, table, lens, i32([n, 0]), refs, moves)
+    pages[33_000] = 7
+    tq.pages_fork(pages, table, lens, refs, i32([0]), i32([1]), moves[:1])
+    assert lens.tolist() == [n, n] and moves[0].tolist() == [33_000, 33_001]
+    assert torch.equal(table[0, :33_001], torch.arange(33_001, dtype=torch.int32, device="cuda"))
+    assert torch.equal(table[1, :33_000], table[0, :33_000]) and int(table[1, 33_000]) == 33_001
+    assert torch.all(refs[:33_000] == 2) and refs[33_000:33_002].tolist() == [1, 1] and not refs[33_002:].any()
+    assert torch.equal(pages[33_001], pages[33_000])
+    # the last entry of a row counts as any other
+    lens.copy_(i32([0, cols * BS]))
+    table[1, cols - 1] = 39_000
+    refs[39_000] = 1
+    tq.pages_resize(pages, table, lens, i32([0, 16]), refs, moves)
+    assert int(refs[39_000]) == 0 and int(table[1, cols - 1]) == -1 and lens.tolist() == [0, 16]
+    assert tq.get_device_error() == 0
