@@ -429,12 +429,21 @@ def _check_codebooks(codebooks: Codebooks, index: int) -> None:
         raise ValueError(f"codebooks on {codebooks.k_centroids.device}, tensors on cuda:{index}")
 
 
+def _check_i32(**numbers) -> None:
+    """Numbers past 32 bits would reach the library cut to their low bits."""
+    for name, n in numbers.items():
+        if not -2**31 <= n < 2**31:
+            raise ValueError(f"{name}={n} does not fit in 32 bits")
+
+
 def paged_attend(out, q, q_starts, pages, block_table, seq_lens, codebooks: Codebooks,
                  sign_seed: int, scale: float, max_q: int, window: int = 0, sinks: int = 0,
                  stream=None) -> None:
     """tq_paged_attend: causal attention of each sequence's last tokens (rows q_starts[b] ..
     q_starts[b + 1] of q, at most max_q) over its packed pages, which hold them already; with
     window > 0 over the last ``window`` tokens and the first ``sinks`` ones."""
+    if (max_q | window | sinks) >> 31:          # negative, or past 32 bits
+        _check_i32(max_q=max_q, window=window, sinks=sinks)
     d, index = _descs(out, q, q_starts, pages, block_table, seq_lens)
     _check_codebooks(codebooks, index)
     _run("tq_paged_attend", index, stream,
@@ -446,6 +455,8 @@ def paged_decode_window(out, q, pages, block_table, seq_lens, codebooks: Codeboo
                         stream=None) -> None:
     """tq_paged_decode_window: one new token a sequence over the last ``window`` packed tokens
     (itself included) and the first ``sinks`` ones."""
+    if (window | sinks) >> 31:
+        _check_i32(window=window, sinks=sinks)
     d, index = _descs(out, q, pages, block_table, seq_lens)
     _check_codebooks(codebooks, index)
     _run("tq_paged_decode_window", index, stream,
@@ -467,6 +478,8 @@ def pages_resize(layers, block_table, seq_lens, new_lens, ref_counts, moves, win
     shared, partly filled last page is copied first), entries released for those that shrink,
     and with window > 0 the pages that a sliding window no longer reaches.  ``layers``: one
     page tensor, or one a model layer."""
+    if (window | sinks) >> 31:
+        _check_i32(window=window, sinks=sinks)
     _run_pages("tq_pages_resize", layers, (block_table, seq_lens, new_lens, ref_counts, moves), stream,
                window, sinks)
 
