@@ -102,3 +102,18 @@ def test_8_bit_keys_that_share_a_direction_in_chunks(d, vb, lens, q_lens, mean):
                                            (256, 3, 4, 40), (128, 4, 4, 40), (64, 4, 3, 80)])
 def test_keys_that_share_a_direction(d, kb, vb, q_len, mean):
     _check_mean_keys(d, 4, 2, kb, vb, [300, 417, 333, 512, 100], [q_len] * 5, mean)
+
+
+@pytest.mark.parametrize("kb", [2, 3, 4, 8])
+@pytest.mark.parametrize("vb", [2, 3, 4, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [12, 40])
+def test_every_width_pair_together(d, kb, vb, q_len):
+    _check_mean_keys(d, 4, 2, kb, vb, [200, 317, 133, 61], [q_len] * 4, 1)
+
+
+@pytest.mark.parametrize("d,hq,hkv,kb,vb,q_lens", [(128, 8, 2, 4, 4, [8, 5]), (128, 8, 2, 4, 2, [100, 41]),
+                                                   (64, 14, 2, 8, 8, [4, 4]), (64, 14, 2, 8, 8, [60, 20]),
+                                                   (256, 4, 2, 3, 4, [16, 9]), (256, 4, 2, 4, 3, [50, 70])])
+def test_long_sequences_together(d, hq, hkv, kb, vb, q_lens):
+    _check_mean_keys(d, hq, hkv, kb, vb, [5001, 2100], q_lens, 3)
