@@ -10,9 +10,12 @@
 
 namespace tq {
 
-// Rows a KV head up to which the rows kernel is used (8 sequences of 4096 tokens, 32/8 heads of
-// 128, 4 bits: 16 rows 31 us against the tiles' 69 us, 64 rows 100 against 69).
-constexpr int kRowsMost = 32;
+// Rows a KV head up to which the rows kernel is used.  us of the rows / tiles kernel, 8 sequences of
+// 4,096 tokens: 16/2 heads of 64, 8/8 bits, 32 rows 26 / 45 (48 rows of 64 sequences of 500 38 / 36);
+// 32/8 heads of 128, 4/4 bits, 32 rows 45 / 82, 48 rows 80 / 81; 16/4 heads of 256, 4/4 bits, where a
+// block takes 8 rows, 16 rows 55 / 61, 24 rows 82 / 61 (and 85 / 64 of 16 windows of 2,048 tokens, 87 /
+// 75 of 64 sequences of 500, but 122 / 173 of one of 32,768).
+constexpr int rows_most(int dim) { return dim == 256 ? 16 : 32; }
 constexpr int kAttendMaxCtas = 8;          // the portable cluster size
 
 // Launches the kernel as clusters of 1 to 8 CTAs that split the keys of a group of rows.  Of the
@@ -158,7 +161,7 @@ TQ_FOR_EACH_DECODE(TQ_DECLARE_TILES)
 TQ_FOR_EACH_DECODE(TQ_DECLARE_ROWS)
 
 inline tq_status launch_attend_any(int dim, int kb, int vb, const AttendParams& p, cudaStream_t st) {
-  const bool tiles = (int64_t)p.max_q * p.group > kRowsMost;
+  const bool tiles = (int64_t)p.max_q * p.group > rows_most(dim);
 #define TQ_ROWS_CASE(D_, KB_)                                                             \
   if (dim == D_ && kb == KB_)                                                             \
     return tiles ? launch_tiles_d##D_##_k##KB_(vb, p, st) : launch_rows_d##D_##_k##KB_(vb, p, st);

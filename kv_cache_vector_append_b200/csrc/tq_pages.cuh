@@ -8,11 +8,11 @@
 // resize and fork plan and allocate in one cluster: it turns the counts into a bitmap of free
 // pages in shared memory (each CTA a contiguous part of the pool), joins the CTAs' totals over
 // distributed shared memory, and lets every free page find its rank (prefix sums of the
-// bitmap's words) and the request of that rank (a search in the prefix sums of the demands).  What follows is long: page copies, shared or released
-// table entries, count updates (integer atomics, so their order does not matter).  Where it is
-// little (see kFusedChunks) the cluster's warps do it themselves after a cluster barrier, else
-// a second launch with a CTA per sequence and layer.  What that needs to know of the plan is
-// in `moves`, a tensor of the caller: {from, to} of a page copy, {-1, -1} for none, {-2, -2}
+// bitmap's words) and the request of that rank (a search in the prefix sums of the demands).  What
+// follows is long: page copies, shared or released table entries, count updates (integer atomics,
+// so their order does not matter).  Where it is little (see kFusedChunks) the cluster's warps do
+// it themselves after a cluster barrier, else a second launch with a CTA per sequence and layer.
+// What that needs to know of the plan is in `moves`, a tensor of the caller: {from, to} of a page copy, {-1, -1} for none, {-2, -2}
 // for a refused request.  No other state is kept between the launches or the calls.
 //
 // Bound: the plan by latency (a few dependent reads and cluster barriers; the pool is read
@@ -34,9 +34,11 @@ constexpr int kPlanMaxCtas = 8;            // portable cluster size
 constexpr int kPagesThreads = 256;
 
 // What the cluster of the plan does itself: at most this many page pieces of kCopyPiece bytes to
-// copy and runs of 128 table entries to go through, four rounds of its 256 warps (a second
-// launch costs more up to there), in at most kFusedLayers layers (a small kernel argument).
-constexpr int kFusedChunks = 1024;
+// copy and runs of 128 table entries to go through, two rounds of its 256 warps, in at most
+// kFusedLayers layers (a small kernel argument).  us on the GPU in one launch / in two, for a pair of
+// calls: 128 runs 22.1 / 22.1, 512 29.4 / 28.8, 1,024 32.3 / 29.5, 1,152 pieces 21.3 / 17.0; from
+// Python, where the host bounds small calls, 288 pieces 30 / 35, 1,024 runs 38.4 / 37.0.
+constexpr int kFusedChunks = 512;
 constexpr int kCopyPiece = 2048;
 constexpr int kFusedLayers = 8;
 

@@ -1,5 +1,5 @@
 """GPU tests of the page operations in the sizes of a whole model: more layers, entries and copies than
-one launch takes (8 layers, 1,024 pieces of 2,048 bytes or runs of 128 table entries)."""
+one launch takes (8 layers, 512 pieces of 2,048 bytes or runs of 128 table entries)."""
 import random
 
 import numpy as np
