@@ -22,9 +22,10 @@
 // packed codes into fp16 tiles in shared memory (lookups of code pairs, one 256-byte row an
 // entry, so that 32 lanes hit 32 banks; the next tile's codes are already on their way into
 // registers), warps 12 and 13 issue the MMAs of a slot each: P V of an item of 64 keys, then Q K
-// of the item after the next, so that a slot's softmax always finds scores.  Both operand tiles are rows of 64 columns with
-// the 128-byte swizzle: K-major for Q K, MN-major for P V, the same bytes.  A cluster of CTAs
-// may split the keys; partials are joined over distributed shared memory as in the rows kernel.
+// of the item after the next, so that a slot's softmax always finds scores.  Both operand tiles
+// are rows of 64 columns with the 128-byte swizzle: K-major for Q K, MN-major for P V, the same
+// bytes.  A cluster of CTAs may split the keys; partials are joined over distributed shared
+// memory as in the rows kernel.
 //
 // Bound: shared memory, which operands (a step of 256 rows x 128 keys reads 256 KB for its
 // MMAs), lookups, tiles and norms share: 830 TFLOP/s on 4,096 new tokens of 20,480 (32/8 heads
@@ -354,13 +355,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const At
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   using C = TilesCfg<D, KB, VB>;
-  constexpr int N = C::N, NI = C::NI, PART = C::PART, E = D / 32;
+  constexpr int N = C::N, NI = C::NI, PART = C::PART;
   constexpr int KPACK = D * KB / 8, VPACK = D * VB / 8;
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* q_s = smem;                                   // [row tile][part][64-column blocks]
   uint8_t* ring_s = smem + C::QBYTES;
   uint8_t* lut = smem + C::OPER;
-  float* norm_s = (float*)(lut + C::LUT);                // [2][K, V][N]
+  float* norm_s = (float*)(lut + C::LUT);                // [buffer][K, V][N]
   TilesMisc* ms = (TilesMisc*)(lut + C::LUT + C::NORMS);
   float* part_s = (float*)smem;                          // [slot][row][PART], at the end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -5,26 +5,30 @@ namespace tq {
 
 namespace {
 
+// At most kFusedLayers layers as a small kernel argument.
+FewLayers few_layers(const PageLayers& layers) {
+  FewLayers few{};
+  few.count = layers.count;
+  for (int l = 0; l < layers.count; ++l) {
+    few.base[l] = layers.base[l];
+    few.blk_stride[l] = layers.blk_stride[l];
+    few.page_bytes[l] = layers.page_bytes[l];
+  }
+  return few;
+}
+
 // The plan runs as one cluster: a CTA per 8192 pages, at most the portable cluster size, which
 // it has where it also does the rest (*fused).
 template <bool FORK>
 tq_status launch_plan(const PlanParams& p, const PageLayers& layers, const DeviceInfo& di,
                       cudaStream_t st, bool* fused) {
-  FewLayers few{};
   int pieces = 1;
   for (int l = 0; l < layers.count; ++l)
     pieces = std::max(pieces, (layers.page_bytes[l] + kCopyPiece - 1) / kCopyPiece);
   *fused = layers.count <= kFusedLayers &&
            (int64_t)p.requests * layers.count * pieces <= kFusedChunks &&
            (int64_t)p.requests * ((p.cols + 127) / 128) <= kFusedChunks;
-  if (*fused) {
-    few.count = layers.count;
-    for (int l = 0; l < layers.count; ++l) {
-      few.base[l] = layers.base[l];
-      few.blk_stride[l] = layers.blk_stride[l];
-      few.page_bytes[l] = layers.page_bytes[l];
-    }
-  }
+  const FewLayers few = *fused ? few_layers(layers) : FewLayers{};
   int ctas = *fused ? kPlanMaxCtas : 1;
   while (ctas < kPlanMaxCtas && (int64_t)ctas * 8192 < p.pool) ctas *= 2;
   const size_t smem = plan_smem(p.pool, ctas, p.requests, FORK ? p.batch : 0);
@@ -83,14 +87,8 @@ tq_status launch_pages_compact(const CompactParams& p, const PageLayers& layers,
   // rows of every layer in 16-byte units where they are multiples of 16 bytes, else 8
   bool wide = true;
   for (int l = 0; l < layers.count; ++l) wide = wide && layers.page_bytes[l] / kPageTokens % 16 == 0;
-  if (layers.count <= kFusedLayers) {      // a small kernel argument
-    FewLayers few{};
-    few.count = layers.count;
-    for (int l = 0; l < layers.count; ++l) {
-      few.base[l] = layers.base[l];
-      few.blk_stride[l] = layers.blk_stride[l];
-      few.page_bytes[l] = layers.page_bytes[l];
-    }
+  if (layers.count <= kFusedLayers) {
+    const FewLayers few = few_layers(layers);
     if (wide) launch_compact_t<uint4>(p, few, grid, st);
     else launch_compact_t<uint2>(p, few, grid, st);
   } else {

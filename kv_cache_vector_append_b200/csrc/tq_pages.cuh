@@ -12,8 +12,9 @@
 // follows is long: page copies, shared or released table entries, count updates (integer atomics,
 // so their order does not matter).  Where it is little (see kFusedChunks) the cluster's warps do
 // it themselves after a cluster barrier, else a second launch with a CTA per sequence and layer.
-// What that needs to know of the plan is in `moves`, a tensor of the caller: {from, to} of a page copy, {-1, -1} for none, {-2, -2}
-// for a refused request.  No other state is kept between the launches or the calls.
+// What that needs to know of the plan is in `moves`, a tensor of the caller: {from, to} of a page
+// copy, {-1, -1} for none, {-2, -2} for a refused request.  No other state is kept between the
+// launches or the calls.
 //
 // Bound: the plan by latency (a few dependent reads and cluster barriers; the pool is read
 // once), the copies and compact by memory bandwidth.

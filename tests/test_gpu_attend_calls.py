@@ -86,3 +86,13 @@ def test_kernels_first_used_inside_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("d,q_lens", [(128, [1, 2]), (64, [4, 3]), (128, [90, 40]), (256, [40, 70])])
+def test_out_may_be_q(d, q_lens):
+    """Every block reads its queries before any row of theirs is written."""
+    tq = _tq()
+    c = Case(tq, d, 8, 2, 4, 4, [2300, 100], q_lens)
+    want = c.run().clone()
+    c.out = c.q
+    assert torch.equal(c.run(), want)
