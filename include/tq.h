@@ -322,12 +322,18 @@ TQ_API tq_status tq_paged_decode_noalloc(tq_tensor out, tq_tensor q, tq_tensor p
  * H_kv; block_size 16; H_kv <= 65535, max_q * H_q / H_kv < 2^22, and B * H_kv * tiles of 8
  * query rows < 2^28 (TQ_ERR_UNSUPPORTED otherwise).
  * The operands of the two contractions are fp16, 8-bit key centroids twice that (hi + lo); sums
- * and softmax statistics are fp32: the result
- * is within about 1e-3 of the exact one in 2-norm (2e-3 where a few keys have very large
- * norms), whatever the type of out.
- * Only tokens a row sees reach its result: whatever the others' norms hold (a stored NaN norm
- * included).  No workspace, no state between calls: calls may overlap on the GPU, and be captured (the
- * library's first call on a device outside any capture).
+ * and softmax statistics are fp32.  Whatever the type of out, all rows together are within about
+ * 1e-3 of the exact result in 2-norm (1,150 random calls: 1.4e-3 at most, in one of 8 rows; 2e-3
+ * where a few keys have very large norms).  A single row may be further off: by 8e-3 of sum_t softmax_t |v_hat_t|, and
+ * where its values cancel by 2e-2 of its own norm.  |q| is summed in fp32: below 1.8e19.
+ * Only tokens a row sees reach its result: whatever the others' norms hold (a stored NaN or
+ * infinite norm included).  out may be q itself.  No workspace, no state between calls: calls may
+ * overlap on the GPU, and be captured (the library's first call on a device outside any capture).
+ * The kernel and, without a window, how many blocks share a sequence's keys are chosen for the
+ * whole call by max_q and block_table's width: give single tokens a call of their own next to long
+ * chunks (2 chunks of 512 and 60 single tokens at 4,096: 553 us in one call, 123 + 121 in two), and
+ * a table view no wider than the longest sequence (8 x 500 tokens in 32 columns 121 us, in 2,048
+ * 203 us).
  * Errors: TQ_ERR_INVALID_ARG / TQ_ERR_UNSUPPORTED (nothing enqueued), TQ_ERR_CUDA. */
 TQ_API tq_status tq_paged_attend(tq_tensor out, tq_tensor q, tq_tensor q_starts, tq_tensor pages,
                                  tq_tensor block_table, tq_tensor seq_lens,
@@ -375,7 +381,8 @@ TQ_API tq_status tq_paged_decode_window(tq_tensor out, tq_tensor q, tq_tensor pa
  * sequence is released), and seq_lens[b] = new_lens[b].
  *   growing    new entries name free pages.  If the sequence's last page is partly filled and
  *              shared (count > 1), it is first replaced by a copy of its own, in every layer.
- *   shrinking  the entries past the new length are released and set to -1.
+ *   shrinking  the entries past the new length are released and set to -1.  (A
+ *              sequence cut back into pages that a window released keeps their -1 entries.)
  *   window > 0 entries of pages that no query at position min(old, new length) or later can
  *              see through a sliding window with sinks (tq_paged_attend) are released too and
  *              set to -1.  The window kernels never read such entries.  0: none.

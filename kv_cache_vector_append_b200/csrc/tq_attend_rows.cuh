@@ -20,9 +20,9 @@
 // those of the cluster's CTAs over distributed shared memory: no workspace, no counters, the
 // same order of sums every time.
 //
-// Bound: instruction issue (some 400 a page) and the L1 wavefronts of loads that touch eight
-// rows each.  64 windows of 4,096 tokens, 28/4 heads of 128, 4/2 bits: 49 us, 2.2 TB/s; a
-// block's start and end take about 8 us of it.
+// Bound: instruction issue (some 350 a page) and the L1 wavefronts of loads that touch eight
+// rows each (75% of the active cycles).  64 windows of 4,096 tokens, 28/4 heads of 128, 4/2 bits:
+// 50 us, 2.2 TB/s; a block's start and end take about 8 us of it.
 #pragma once
 
 #include <cooperative_groups.h>

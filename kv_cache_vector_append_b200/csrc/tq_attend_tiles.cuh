@@ -28,8 +28,8 @@
 // memory as in the rows kernel.
 //
 // Bound: shared memory, which operands (a step of 256 rows x 128 keys reads 256 KB for its
-// MMAs), lookups, tiles and norms share: 830 TFLOP/s on 4,096 new tokens of 20,480 (32/8 heads
-// of 128, 4/4 bits, 1,490 us), half of the measured matrix rate; the MMAs alone run at 1,267.
+// MMAs), lookups, tiles and norms share: 805 TFLOP/s on 4,096 new tokens of 20,480 (32/8 heads
+// of 128, 4/4 bits, 1,537 us), half of the measured matrix rate; the MMAs alone run at 1,267.
 // Without the dequantization it took 9% less, without the softmax 14% less; no single part of
 // the softmax is worth more than 5%.
 #pragma once
